@@ -527,6 +527,138 @@ kvtc_status kvtc_pq_decode(kvtc_plan_t plan, const kvtc_pq_config* q, const floa
                            size_t outlier_slots, int32_t T, void* v_out, int32_t out_dtype, void* ws, size_t ws_bytes,
                            uint32_t* status_dev, hipStream_t stream);
 
+/* ---- microscaled paged cache: write, read, attention --------------------- */
+
+/* A cache that is quantised as it is written and attended to where it lies.
+ * Keys and values sit in pages of 16 tokens (the page of the paged batches
+ * above) as microscaled floating point: elements of 4 bits (E2M1) or 8 bits
+ * (E4M3), keys and values each in a width of their own, with one
+ * power-of-two scale (E8M0) per token, head and 32 channels.
+ *
+ * Quantising a block of 32 channels with a = max|x|: the scale is 2^e with
+ * the smallest e for which a rounds to a finite element, a < 7 2^e (E2M1,
+ * largest element 6) or a < 464 2^e (E4M3, 448), e clamped to [-112, 125]
+ * (E2M1) or [-112, 119] (E4M3); elements are x 2^-e rounded to nearest even,
+ * saturating at the clamp.  So no element is off by more than half a step of
+ * its grid, and every value of the cache is a bf16 number.  A block with a
+ * NaN or an infinity is stored as NaN (scale byte 255) and reported.
+ *
+ * Pool (device, kvtc_mx_pool_size() bytes, 16-byte aligned): records
+ * [layers][pool_pages][kv_heads], one record per page and head, laid out in
+ * the order in which the matrix instructions of the attention take it:
+ *   key codes     [16 tokens][head_dim bits_k / 8 bytes], channel order
+ *   value codes   [4 groups of 4 tokens][16][4 tokens][head_dim / 16
+ *                 channels]: entry n of a group holds channels
+ *                 n head_dim / 16 ... of its four tokens
+ *   key scales    [16 tokens][head_dim / 32] bytes e + 127
+ *   value scales  [4 groups][head_dim / 32][4 tokens] bytes e + 127
+ * 4-bit codes fill bytes from the low nibble up (sign, 2 exponent bits,
+ * 1 mantissa bit).  Pool bytes that no call wrote may hold anything.
+ *
+ * A batch is n_seqs ragged sequences.  Sequence z has kv_lens[z] tokens,
+ * token t in page page_table[z max_pages + t / 16], row t % 16; its rows in
+ * the call's tensors are row_start[z] .. row_start[z + 1] - 1, and they are
+ * its LAST tokens: row i of n stands at position kv_lens[z] - n + i.  So a
+ * step that appends one token has one row a sequence, a prompt has all of
+ * them, and kv_lens counts the tokens after the write.  A sequence may have
+ * no rows; positions below 0 (more rows than tokens) are skipped when
+ * writing and reading, and are empty rows of the attention.  Tensor rows
+ * that belong to no sequence are left as they are.
+ *
+ * The three arrays are device memory and only the bounds are the host's, so
+ * a captured call can be replayed with other lengths and pages within them.
+ * The device checks what it reads: a length or row range outside the bounds
+ * makes the call skip that sequence, a page index outside the pool skips
+ * that page's tokens (the attention takes them as masked), and either sets
+ * bit KVTC_ERR_INVALID_ARG in *status_dev.  status_dev (device, 4-byte
+ * aligned, may be NULL) is only OR-ed into and never cleared by these calls:
+ * a serving loop reads it when it likes.  Two sequences may name the same
+ * page to read from it; a page that two tokens of one write fall into the
+ * same row of is the caller's error and holds either's bytes.
+ *
+ * Row tensors (keys, values, queries) are head_dim contiguous elements per
+ * row and head; strides are in elements and may be any multiple of 16 bytes
+ * (0 too, for inputs).  All calls are asynchronous on `stream`, allocate
+ * nothing and may be captured into a graph. */
+enum { KVTC_MX_PAGE = 16 };
+
+typedef struct kvtc_mx_config {
+  int32_t layers, kv_heads, head_dim; /* head_dim 64 or 128; layers kv_heads <= 65536 */
+  int32_t dtype;                      /* KVTC_BF16 or KVTC_FP32: rows written, queries and attention outputs */
+  int32_t bits_k, bits_v;             /* 4 (E2M1) or 8 (E4M3) */
+  int32_t pool_pages;
+} kvtc_mx_config;
+
+typedef struct kvtc_mx_batch {
+  int32_t n_seqs;
+  int32_t max_pages;         /* columns of the page table */
+  int32_t total_rows;        /* rows of the call's tensors */
+  int32_t max_rows;          /* bound on a sequence's rows */
+  int32_t max_len;           /* bound on kv_lens, at most 16 max_pages and 2^30 */
+  int32_t reserved;          /* 0 */
+  const int32_t* page_table; /* device [n_seqs][max_pages] */
+  const int32_t* kv_lens;    /* device [n_seqs] */
+  const int32_t* row_start;  /* device [n_seqs + 1], non-decreasing */
+} kvtc_mx_batch;
+
+/* Bytes of one record (page and head) and of the whole pool (host only). */
+kvtc_status kvtc_mx_pool_size(const kvtc_mx_config* cfg, size_t* record_bytes, size_t* pool_bytes);
+
+/* Quantise the batch's rows of layers [layer, layer + n_layers) into their
+ * pages.  k, v: device, cfg->dtype, element (l, h, r, c) at
+ * l strides[0] + h strides[1] + r strides[2] + c with l counted from
+ * `layer`, so that both a layer's [rows, heads, head_dim] slices and a
+ * decoded cache [L, H, T, D] (kvtc_decode) are written as they lie.  Bytes
+ * of other tokens stay as they are.  A block with a NaN or an infinity sets
+ * bit KVTC_ERR_NONFINITE.  Errors: INVALID_ARG, UNSUPPORTED, CAPACITY
+ * (pool_bytes too small), HIP. */
+kvtc_status kvtc_mx_write(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                          const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                          void* pool, size_t pool_bytes, uint32_t* status_dev, hipStream_t stream);
+
+/* Read the batch's rows back into k_out, v_out (device, out_dtype KVTC_BF16
+ * or KVTC_FP32; exact in both), laid out as in kvtc_mx_write; a sequence
+ * read into [L, H, T, D] is what kvtc_encode takes.  Output strides must not
+ * make elements overlap (INVALID_ARG). */
+kvtc_status kvtc_mx_read(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                         const void* pool, size_t pool_bytes, void* k_out, const int64_t* k_strides, void* v_out,
+                         const int64_t* v_strides, int32_t out_dtype, uint32_t* status_dev, hipStream_t stream);
+
+/* Workspace bytes of kvtc_mx_attn (shared_pages 0) or kvtc_mx_attn_shared
+ * for this batch's bounds; may be 0.  Every concurrent call needs its own. */
+kvtc_status kvtc_mx_attn_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t q_heads,
+                                   int32_t shared_pages, size_t* ws_bytes);
+
+/* Attention of the batch's rows over one layer of the cache:
+ *   s_t = scale q . k_t over the tokens t < lim, lim = position + 1 when
+ *   causal, else kv_lens[z];  out = sum_t softmax(s)_t v_t;
+ *   lse = ln sum_t exp(s_t).
+ * q: device, cfg->dtype, q_heads heads (a multiple of kv_heads; head h reads
+ * kv head h / (q_heads / kv_heads)), row r of head h at r q_stride +
+ * h head_dim.  out: device [total_rows, q_heads, head_dim] in cfg->dtype;
+ * lse: device fp32 [total_rows, q_heads] or NULL.  A row that attends to
+ * nothing gets zeros and lse -infinity.  scale must be finite and positive.
+ * A NaN token affects the rows that attend to it and no others.
+ *
+ * Products are exact (bf16 queries) and summed in fp32, the softmax is fp32;
+ * the weights are rounded to bf16 before they meet the values, as the output
+ * is.  fp32 queries and weights are split into three bf16 parts that keep
+ * 24 bits.  Deterministic. */
+kvtc_status kvtc_mx_attn(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,
+                         size_t pool_bytes, const void* q, int64_t q_stride, int32_t q_heads, float scale,
+                         int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status_dev,
+                         hipStream_t stream);
+
+/* kvtc_mx_attn for a batch whose sequences share their first shared_pages
+ * pages (0 <= shared_pages <= max_pages): the shared tokens are read, and
+ * multiplied with the rows of all sequences, once, through the first
+ * sequence's page table; the other sequences' entries for them are not read.
+ * Sequences shorter than the prefix attend to their own first tokens of it. */
+kvtc_status kvtc_mx_attn_shared(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer,
+                                const void* pool, size_t pool_bytes, int32_t shared_pages, const void* q,
+                                int64_t q_stride, int32_t q_heads, float scale, int32_t causal, void* out, float* lse,
+                                void* ws, size_t ws_bytes, uint32_t* status_dev, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,287 @@
+// C ABI of the microscaled paged cache: argument checks, the split of the
+// attention over workgroups, and the launch sequences.
+#include <math.h>
+
+#include <algorithm>
+#include <utility>
+
+#include "mx_internal.h"
+
+using namespace kvtc;
+
+namespace {
+
+constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of 256 threads in a launch
+
+bool misaligned(const void* p, unsigned to = 16) { return ((uintptr_t)p & (to - 1)) != 0; }
+
+kvtc_status check_config(const kvtc_mx_config* c) {
+  if (!c) return KVTC_ERR_INVALID_ARG;
+  if (c->layers < 1 || c->kv_heads < 1 || c->pool_pages < 1) return KVTC_ERR_INVALID_ARG;
+  if (c->dtype != KVTC_BF16 && c->dtype != KVTC_FP32) return KVTC_ERR_INVALID_ARG;
+  if ((c->bits_k != 4 && c->bits_k != 8) || (c->bits_v != 4 && c->bits_v != 8)) return KVTC_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return KVTC_ERR_UNSUPPORTED;
+  if ((int64_t)c->layers * c->kv_heads > 65536) return KVTC_ERR_UNSUPPORTED;
+  return KVTC_OK;
+}
+
+int64_t layer_bytes(const kvtc_mx_config& c) {
+  return (int64_t)c.pool_pages * c.kv_heads * mx_record(c.head_dim, c.bits_k, c.bits_v).bytes;
+}
+
+kvtc_status check_batch(const kvtc_mx_batch* b) {
+  if (!b || b->reserved != 0) return KVTC_ERR_INVALID_ARG;
+  if (b->n_seqs < 0 || b->max_pages < 1 || b->total_rows < 0 || b->max_rows < 0 || b->max_len < 0)
+    return KVTC_ERR_INVALID_ARG;
+  if ((int64_t)b->max_len > (int64_t)b->max_pages * KVTC_MX_PAGE || b->max_len > (1 << 30)) return KVTC_ERR_INVALID_ARG;
+  if (b->n_seqs > 0 && (!b->page_table || !b->kv_lens || !b->row_start)) return KVTC_ERR_INVALID_ARG;
+  if (misaligned(b->page_table, 4) || misaligned(b->kv_lens, 4) || misaligned(b->row_start, 4))
+    return KVTC_ERR_INVALID_ARG;
+  return KVTC_OK;
+}
+
+bool nothing_to_do(const kvtc_mx_batch& b) { return b.n_seqs == 0 || b.total_rows == 0 || b.max_rows == 0; }
+
+// Configuration, batch, pool and status, common to every call; *layer is the
+// first record of `layer`.
+kvtc_status check_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                       const void* pool, size_t pool_bytes, const uint32_t* status, uint8_t** first) {
+  kvtc_status st = check_config(cfg);
+  if (st != KVTC_OK) return st;
+  st = check_batch(batch);
+  if (st != KVTC_OK) return st;
+  if (layer < 0 || n_layers < 1 || n_layers > cfg->layers || layer > cfg->layers - n_layers) return KVTC_ERR_INVALID_ARG;
+  if (!pool || misaligned(pool) || misaligned(status, 4)) return KVTC_ERR_INVALID_ARG;
+  if (pool_bytes / (size_t)cfg->layers < (size_t)layer_bytes(*cfg)) return KVTC_ERR_CAPACITY;
+  *first = (uint8_t*)const_cast<void*>(pool) + layer * layer_bytes(*cfg);
+  return KVTC_OK;
+}
+
+// Strides of a row tensor: whole 16 bytes, none negative; of an output also
+// such that no two elements fall together (each stride passes the span of
+// the smaller ones).
+bool bad_strides(const int64_t* st, const int64_t (&extent)[3], int D, int elem, bool out) {
+  if (!st) return true;
+  for (int i = 0; i < 3; ++i)
+    if (st[i] < 0 || st[i] > ((int64_t)1 << 46) || (st[i] * elem) % 16) return true;
+  if (!out) return false;
+  std::pair<int64_t, int64_t> d[3];
+  for (int i = 0; i < 3; ++i) d[i] = {st[i], extent[i]};
+  std::sort(d, d + 3);
+  int64_t span = D;
+  for (const auto& [s, n] : d) {
+    if (n < 2) continue;
+    if (s < span) return true;
+    span += s * (n - 1);
+  }
+  return false;
+}
+
+kvtc_status io_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t layer, int32_t n_layers, void* k,
+                    const int64_t* ks, void* v, const int64_t* vs, const void* pool, size_t pool_bytes, int32_t dtype,
+                    uint32_t* status, bool write, hipStream_t stream) {
+  uint8_t* first;
+  const kvtc_status st = check_call(cfg, b, layer, n_layers, pool, pool_bytes, status, &first);
+  if (st != KVTC_OK) return st;
+  if (dtype != KVTC_BF16 && dtype != KVTC_FP32) return KVTC_ERR_INVALID_ARG;
+  const int64_t extent[3] = {n_layers, cfg->kv_heads, b->total_rows};
+  const int elem = dtype == KVTC_BF16 ? 2 : 4;
+  if (bad_strides(ks, extent, cfg->head_dim, elem, !write) || bad_strides(vs, extent, cfg->head_dim, elem, !write))
+    return KVTC_ERR_INVALID_ARG;
+  if (nothing_to_do(*b)) return KVTC_OK;
+  if (!k || !v || misaligned(k) || misaligned(v)) return KVTC_ERR_INVALID_ARG;
+  MxIoParams p{};
+  p.b = *b;
+  p.H = cfg->kv_heads;
+  p.pool_pages = cfg->pool_pages;
+  p.n_layers = n_layers;
+  p.pool = first;
+  p.layer_bytes = layer_bytes(*cfg);
+  p.x[0] = k;
+  p.x[1] = v;
+  for (int i = 0; i < 3; ++i) {
+    p.st[0][i] = ks[i];
+    p.st[1][i] = vs[i];
+  }
+  p.status = status;
+  // n rows that start anywhere in a page touch at most ceil((n + 15) / 16) pages
+  const int64_t rows = std::min({b->max_rows, b->total_rows, b->max_len});
+  const int64_t units = std::max<int64_t>((rows + 2 * KVTC_MX_PAGE - 2) / KVTC_MX_PAGE, 1);
+  if (units * b->n_seqs > kMaxGrid) return KVTC_ERR_UNSUPPORTED;
+  p.n_units = (int32_t)units;
+  const hipError_t e = write ? launch_mx_write(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, dtype == KVTC_FP32, stream)
+                             : launch_mx_read(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, dtype == KVTC_FP32, stream);
+  return e == hipSuccess ? KVTC_OK : KVTC_ERR_HIP;
+}
+
+// How one pass of the attention is cut up.
+struct Cut {
+  int nt;           // 16-row tiles of a workgroup
+  int64_t tiles;    // workgroups along the rows
+  int nsplit, chunk;  // workgroups along the tokens, tokens of each
+};
+Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span, bool f32) {
+  Cut c{};
+  c.nt = rows <= 16 ? 1 : rows <= 32 || f32 ? 2 : 4;
+  c.tiles = (rows + 16 * c.nt - 1) / (16 * c.nt);
+  // enough workgroups to fill the card four deep, none with fewer than 256 tokens
+  const int64_t units = c.tiles * H * seqs, want = (1024 + units - 1) / units;
+  const int64_t n = std::max<int64_t>(1, std::min(want, (span + 255) / 256));
+  c.chunk = (int)(((span + n - 1) / n + 127) / 128 * 128);
+  c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / std::max(c.chunk, 1));
+  return c;
+}
+
+struct AttnPlan {
+  Cut prefix, own;  // nsplit 0: no such pass
+  int begin;        // first token of `own`
+  int64_t slots, ws;
+};
+
+kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q_heads, int32_t shared, AttnPlan* a) {
+  if (q_heads < c.kv_heads || q_heads % c.kv_heads) return KVTC_ERR_INVALID_ARG;
+  if (shared < 0 || shared > b.max_pages) return KVTC_ERR_INVALID_ARG;
+  if ((int64_t)b.total_rows * q_heads > 0x7FFFFFFF) return KVTC_ERR_UNSUPPORTED;
+  *a = AttnPlan{};
+  if (nothing_to_do(b)) return KVTC_OK;
+  const int G = q_heads / c.kv_heads;
+  const bool f32 = c.dtype == KVTC_FP32;
+  a->begin = (int)std::min<int64_t>((int64_t)shared * KVTC_MX_PAGE, b.max_len);
+  const int64_t rows = (int64_t)std::min(b.max_rows, b.total_rows) * G;
+  if (a->begin < b.max_len || a->begin == 0) a->own = cut_pass(rows, b.n_seqs, c.kv_heads, b.max_len - a->begin, f32);
+  if (a->begin > 0) a->prefix = cut_pass((int64_t)b.total_rows * G, 1, c.kv_heads, a->begin, f32);
+  a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
+  a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
+  if (a->own.tiles * c.kv_heads * std::max(a->own.nsplit, 1) * b.n_seqs > kMaxGrid ||
+      a->prefix.tiles * c.kv_heads * std::max(a->prefix.nsplit, 1) > kMaxGrid ||
+      ((int64_t)b.total_rows * q_heads + 3) / 4 > kMaxGrid)
+    return KVTC_ERR_UNSUPPORTED;
+  return KVTC_OK;
+}
+
+kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t layer, const void* pool,
+                      size_t pool_bytes, int32_t shared, const void* q, int64_t q_stride, int32_t q_heads, float scale,
+                      int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status,
+                      hipStream_t stream) {
+  uint8_t* first;
+  kvtc_status st = check_call(cfg, b, layer, 1, pool, pool_bytes, status, &first);
+  if (st != KVTC_OK) return st;
+  AttnPlan a;
+  st = plan_attn(*cfg, *b, q_heads, shared, &a);
+  if (st != KVTC_OK) return st;
+  const int elem = cfg->dtype == KVTC_BF16 ? 2 : 4;
+  if (!(scale > 0.0f) || !isfinite(scale) || (causal != 0 && causal != 1)) return KVTC_ERR_INVALID_ARG;
+  if (q_stride < 0 || q_stride > ((int64_t)1 << 46) || (q_stride * elem) % 16) return KVTC_ERR_INVALID_ARG;
+  if (nothing_to_do(*b)) return KVTC_OK;
+  if (!q || !out || misaligned(q) || misaligned(out) || misaligned(lse, 4) || misaligned(ws)) return KVTC_ERR_INVALID_ARG;
+  if (a.ws > 0 && !ws) return KVTC_ERR_INVALID_ARG;
+  if ((int64_t)ws_bytes < a.ws) return KVTC_ERR_CAPACITY;
+  const bool f32 = cfg->dtype == KVTC_FP32;
+  MxAttnParams p{};
+  p.b = *b;
+  p.pool = first;
+  p.pool_pages = cfg->pool_pages;
+  p.H = cfg->kv_heads;
+  p.G = q_heads / cfg->kv_heads;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.c = (float)((double)scale * 1.4426950408889634);
+  p.causal = causal;
+  p.out = out;
+  p.lse = lse;
+  p.status = status;
+  if (a.slots) {
+    p.ws_o = (float*)ws;
+    p.ws_ml = (float2*)(p.ws_o + a.slots * b->total_rows * q_heads * (int64_t)cfg->head_dim);
+  }
+  auto pass = [&](const Cut& c) {
+    p.tiles = (int32_t)c.tiles;
+    p.nsplit = c.nsplit;
+    p.chunk = c.chunk;
+    return launch_mx_attn(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, f32, c.nt, stream);
+  };
+  if (a.prefix.nsplit) {
+    p.prefix = 1;
+    p.end = a.begin;
+    if (pass(a.prefix) != hipSuccess) return KVTC_ERR_HIP;
+    p.prefix = 0;
+  }
+  p.begin = a.begin;
+  p.end = 0x7FFFFFFF;
+  p.slot0 = a.prefix.nsplit;
+  if (a.own.nsplit && pass(a.own) != hipSuccess) return KVTC_ERR_HIP;
+  if (!a.slots) return KVTC_OK;
+  MxJoinParams j{};
+  j.b = *b;
+  j.Hq = q_heads;
+  j.D = cfg->head_dim;
+  j.causal = causal;
+  j.begin = a.begin;
+  j.prefix_splits = a.prefix.nsplit;
+  j.prefix_chunk = a.prefix.chunk;
+  j.nsplit = a.own.nsplit;
+  j.chunk = std::max(a.own.chunk, 1);
+  j.ws_o = p.ws_o;
+  j.ws_ml = p.ws_ml;
+  j.out = out;
+  j.lse = lse;
+  j.status = status;
+  return launch_mx_join(j, f32, stream) == hipSuccess ? KVTC_OK : KVTC_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvtc_status kvtc_mx_pool_size(const kvtc_mx_config* cfg, size_t* record_bytes, size_t* pool_bytes) {
+  const kvtc_status st = check_config(cfg);
+  if (st != KVTC_OK) return st;
+  if (!record_bytes || !pool_bytes) return KVTC_ERR_INVALID_ARG;
+  *record_bytes = (size_t)mx_record(cfg->head_dim, cfg->bits_k, cfg->bits_v).bytes;
+  *pool_bytes = (size_t)cfg->layers * (size_t)layer_bytes(*cfg);
+  return KVTC_OK;
+}
+
+kvtc_status kvtc_mx_write(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                          const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                          void* pool, size_t pool_bytes, uint32_t* status_dev, hipStream_t stream) {
+  return io_call(cfg, batch, layer, n_layers, const_cast<void*>(k), k_strides, const_cast<void*>(v), v_strides, pool,
+                 pool_bytes, cfg ? cfg->dtype : 0, status_dev, true, stream);
+}
+
+kvtc_status kvtc_mx_read(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                         const void* pool, size_t pool_bytes, void* k_out, const int64_t* k_strides, void* v_out,
+                         const int64_t* v_strides, int32_t out_dtype, uint32_t* status_dev, hipStream_t stream) {
+  return io_call(cfg, batch, layer, n_layers, k_out, k_strides, v_out, v_strides, pool, pool_bytes, out_dtype,
+                 status_dev, false, stream);
+}
+
+kvtc_status kvtc_mx_attn_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t q_heads,
+                                   int32_t shared_pages, size_t* ws_bytes) {
+  kvtc_status st = check_config(cfg);
+  if (st == KVTC_OK) st = check_batch(batch);
+  if (st != KVTC_OK) return st;
+  if (!ws_bytes) return KVTC_ERR_INVALID_ARG;
+  AttnPlan a;
+  st = plan_attn(*cfg, *batch, q_heads, shared_pages, &a);
+  if (st == KVTC_OK) *ws_bytes = (size_t)a.ws;
+  return st;
+}
+
+kvtc_status kvtc_mx_attn(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,
+                         size_t pool_bytes, const void* q, int64_t q_stride, int32_t q_heads, float scale,
+                         int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status_dev,
+                         hipStream_t stream) {
+  return attn_call(cfg, batch, layer, pool, pool_bytes, 0, q, q_stride, q_heads, scale, causal, out, lse, ws, ws_bytes,
+                   status_dev, stream);
+}
+
+kvtc_status kvtc_mx_attn_shared(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer,
+                                const void* pool, size_t pool_bytes, int32_t shared_pages, const void* q,
+                                int64_t q_stride, int32_t q_heads, float scale, int32_t causal, void* out, float* lse,
+                                void* ws, size_t ws_bytes, uint32_t* status_dev, hipStream_t stream) {
+  return attn_call(cfg, batch, layer, pool, pool_bytes, shared_pages, q, q_stride, q_heads, scale, causal, out, lse,
+                   ws, ws_bytes, status_dev, stream);
+}
+
+}  // extern "C"

@@ -54,6 +54,18 @@ class PqConfig(ctypes.Structure):
                 ("outliers", ctypes.c_int32), ("block_tokens", ctypes.c_int32)]
 
 
+class MxConfig(ctypes.Structure):
+    _fields_ = [("layers", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("bits_k", ctypes.c_int32), ("bits_v", ctypes.c_int32),
+                ("pool_pages", ctypes.c_int32)]
+
+
+class MxBatchStruct(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("total_rows", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("max_len", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("row_start", ctypes.c_void_p)]
+
+
 def make_pq_config(pq: dict) -> PqConfig:
     return PqConfig(pq["sub_dim"], pq["k1"], pq["k2"], pq["outliers"], pq["block_tokens"])
 
@@ -142,6 +154,26 @@ EXPORTS = {
     "kvtc_sq_decode": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "kvtc_mx_pool_size": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t),
+                                         ctypes.POINTER(ctypes.c_size_t)]),
+    "kvtc_mx_write": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvtc_mx_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                    ctypes.c_void_p]),
+    "kvtc_mx_attn_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.POINTER(ctypes.c_size_t)]),
+    "kvtc_mx_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                    ctypes.c_size_t, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                                    ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvtc_mx_attn_shared": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                           ctypes.c_size_t, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.c_int32, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                           ctypes.c_void_p]),
 }
 
 _lib = None
@@ -513,6 +545,180 @@ class Plan:
         self.pq_decode_async(pq, cb1, cb2, codes.contiguous(), rms.contiguous(), o, T, v_out, ws, status, out_dtype)
         torch.cuda.synchronize(self.device)
         return v_out, int(status[0].item())
+
+
+# ---- microscaled paged cache (kvtc_mx_*)
+
+
+class MxBatch:
+    """A ragged batch of sequences of an MxCache: device int32 arrays (kept
+    alive here) and the host's bounds on what they hold.  The arrays may be
+    changed in place between calls, within the bounds."""
+
+    def __init__(self, page_table: torch.Tensor, kv_lens: torch.Tensor, row_start: torch.Tensor, total_rows: int,
+                 max_rows: int, max_len: int):
+        n = kv_lens.numel()
+        for t, shape in ((page_table, (n, page_table.shape[-1])), (kv_lens, (n,)), (row_start, (n + 1,))):
+            if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError("page_table [n, pages], kv_lens [n] and row_start [n + 1] are contiguous int32")
+        self.page_table, self.kv_lens, self.row_start = page_table, kv_lens, row_start
+        self.total_rows, self.max_rows, self.max_len = total_rows, max_rows, max_len
+        self._c = MxBatchStruct(n, page_table.shape[1], total_rows, max_rows, max_len, 0, page_table.data_ptr(),
+                                kv_lens.data_ptr(), row_start.data_ptr())
+        self.ref = ctypes.byref(self._c)
+
+
+class MxCache:
+    """A microscaled paged cache: configuration and pool (uint8 [layers,
+    pool_pages, kv_heads, record bytes], allocated here unless given).
+
+    cfg: layers, kv_heads, head_dim, dtype (FP32 / BF16), bits_k and bits_v
+    (4 or 8).  Calls run on the current stream of the cache's device, or on
+    `stream`; `status` is an int32 tensor whose first word they OR into."""
+
+    def __init__(self, cfg: dict, pool_pages: int, device="cuda", pool: torch.Tensor | None = None):
+        self.cfg = dict(cfg)
+        self._c = MxConfig(cfg["layers"], cfg["kv_heads"], cfg["head_dim"], cfg["dtype"], cfg["bits_k"],
+                           cfg["bits_v"], pool_pages)
+        self._ref = ctypes.byref(self._c)
+        rec, total = ctypes.c_size_t(0), ctypes.c_size_t(0)
+        _check(lib().kvtc_mx_pool_size(self._ref, ctypes.byref(rec), ctypes.byref(total)), "kvtc_mx_pool_size")
+        self.record_bytes, self.pool_bytes = rec.value, total.value
+        shape = (cfg["layers"], pool_pages, cfg["kv_heads"], rec.value)
+        if pool is None:
+            pool = torch.empty(shape, dtype=torch.uint8, device=device)
+        if pool.dtype != torch.uint8 or tuple(pool.shape) != shape or not pool.is_contiguous():
+            raise ValueError(f"the pool is a contiguous uint8 tensor of shape {shape}")
+        self.pool, self.pool_pages, self.device = pool, pool_pages, pool.device
+        self.dtype = torch.float32 if cfg["dtype"] == FP32 else torch.bfloat16
+        self._head = (cfg["kv_heads"], cfg["head_dim"])
+        self._pool_ptr = pool.data_ptr()
+
+    def batch(self, page_table, kv_lens, row_start, total_rows: int, max_rows: int, max_len: int) -> MxBatch:
+        """The batch over device arrays; see MxBatch and kvtc_mx_batch."""
+        for t in (page_table, kv_lens, row_start):
+            self._own(t)
+        return MxBatch(page_table, kv_lens, row_start, total_rows, max_rows, max_len)
+
+    def _own(self, t):
+        if t.device != self.device:
+            raise ValueError(f"a tensor on {t.device} for a cache on {self.device}")
+
+    def _call(self, fn, stream, *args):
+        """Runs a library call with the cache's device current."""
+        if torch.cuda.current_device() == self.device.index:
+            s = stream if stream is not None else torch.cuda.current_stream()
+            st = fn(*args, s.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                s = stream if stream is not None else torch.cuda.current_stream()
+                st = fn(*args, s.cuda_stream)
+        if st != OK:
+            raise KvtcError(st, fn.__name__)
+
+    def _rows(self, x, batch, n_layers):
+        """(pointer, strides) of a row tensor [rows, heads, head_dim] or
+        [layers, heads, rows, head_dim]."""
+        if x.device != self.device:
+            self._own(x)
+        sh = x.shape
+        st = [t if d > 1 else 0 for t, d in zip(x.stride()[:-1], sh)] + [x.stride(-1)]
+        if len(sh) == 3:
+            ok = n_layers == 1 and sh == (batch.total_rows, *self._head)
+            strides = (0, st[1], st[0])
+        else:
+            ok = len(sh) == 4 and sh == (n_layers, self._head[0], batch.total_rows, self._head[1])
+            strides = st[:3] if ok else None
+        if not ok or st[-1] != 1:
+            raise ValueError("rows are [total_rows, kv_heads, head_dim] of one layer or [layers, kv_heads, "
+                             "total_rows, head_dim], with the channels contiguous")
+        return x.data_ptr(), (ctypes.c_int64 * 3)(*strides)
+
+    @staticmethod
+    def _status(status):
+        if status is None:
+            return None
+        if status.dtype != torch.int32 or status.numel() < 1:
+            raise ValueError("status is an int32 tensor")
+        return status.data_ptr()
+
+    def write(self, batch: MxBatch, k: torch.Tensor, v: torch.Tensor, layer: int = 0,
+              status: torch.Tensor | None = None, stream=None):
+        """kvtc_mx_write: k, v [total_rows, kv_heads, head_dim] of one layer,
+        or [n, kv_heads, total_rows, head_dim] of the layers from `layer`."""
+        if k.dtype != self.dtype or v.dtype != self.dtype:
+            raise ValueError(f"keys and values are {self.dtype}")
+        n = k.shape[0] if k.dim() == 4 else 1
+        (kp, ks), (vp, vs) = self._rows(k, batch, n), self._rows(v, batch, n)
+        self._call(lib().kvtc_mx_write, stream, self._ref, batch.ref, layer, n, kp, ks, vp, vs, self._pool_ptr,
+                   self.pool_bytes, self._status(status))
+
+    def read(self, batch: MxBatch, k_out: torch.Tensor, v_out: torch.Tensor, layer: int = 0,
+             status: torch.Tensor | None = None, stream=None):
+        """kvtc_mx_read into k_out, v_out (bf16 or fp32, shaped as in write);
+        returns them."""
+        if k_out.dtype != v_out.dtype or k_out.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("outputs are both bfloat16 or both float32")
+        n = k_out.shape[0] if k_out.dim() == 4 else 1
+        (kp, ks), (vp, vs) = self._rows(k_out, batch, n), self._rows(v_out, batch, n)
+        self._call(lib().kvtc_mx_read, stream, self._ref, batch.ref, layer, n, self._pool_ptr, self.pool_bytes, kp,
+                   ks, vp, vs, BF16 if k_out.dtype == torch.bfloat16 else FP32, self._status(status))
+        return k_out, v_out
+
+    def workspace(self, batch: MxBatch, q_heads: int, shared_pages: int = 0) -> torch.Tensor:
+        """A workspace for the attention of this batch's bounds."""
+        n = ctypes.c_size_t(0)
+        _check(lib().kvtc_mx_attn_workspace(self._ref, batch.ref, q_heads, shared_pages, ctypes.byref(n)),
+               "kvtc_mx_attn_workspace")
+        return torch.empty(max(n.value, 16), dtype=torch.uint8, device=self.device)
+
+    def _attention(self, batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream):
+        if q.device != self.device:
+            self._own(q)
+        heads, D = q.shape[1], self._head[1]
+        if q.dtype != self.dtype or q.dim() != 3 or q.shape[0] != batch.total_rows or q.shape[2] != D or \
+                q.stride(2) != 1 or (q.stride(1) != D and heads > 1):
+            raise ValueError(f"queries are {self.dtype} [total_rows, heads, {D}] with contiguous heads")
+        if out is None or ws is None:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+                if out is None:
+                    out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+                if ws is None:
+                    ws = self.workspace(batch, heads, shared_pages or 0)
+        if out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != self.device:
+            raise ValueError("out is a contiguous tensor of the queries' type and shape")
+        lp = None
+        if lse is not None:
+            if lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or \
+                    lse.device != self.device:
+                raise ValueError("lse is a contiguous float32 tensor [total_rows, heads]")
+            lp = lse.data_ptr()
+        if ws.device != self.device or not ws.is_contiguous():
+            raise ValueError("the workspace is a contiguous tensor on the cache's device")
+        tail = (q.data_ptr(), q.stride(0) if q.shape[0] > 1 else 0, heads, scale if scale is not None else D ** -0.5, 1 if causal else 0,
+                out.data_ptr(), lp, ws.data_ptr(), ws.nbytes, self._status(status))
+        if shared_pages is None:
+            self._call(lib().kvtc_mx_attn, stream, self._ref, batch.ref, layer, self._pool_ptr, self.pool_bytes, *tail)
+        else:
+            self._call(lib().kvtc_mx_attn_shared, stream, self._ref, batch.ref, layer, self._pool_ptr,
+                       self.pool_bytes, shared_pages, *tail)
+        return (out, lse) if lse is not None else out
+
+    def attention(self, batch: MxBatch, q: torch.Tensor, scale: float | None = None, causal: bool = True,
+                  layer: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                  ws: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+        """kvtc_mx_attn: q [total_rows, q_heads, head_dim] -> out, or (out,
+        lse) when lse is given.  scale defaults to head_dim ** -0.5.  out and
+        ws are allocated on the call's stream when not given."""
+        return self._attention(batch, q, None, scale, causal, layer, out, lse, ws, status, stream)
+
+    def attention_shared(self, batch: MxBatch, q: torch.Tensor, shared_pages: int, scale: float | None = None,
+                         causal: bool = True, layer: int = 0, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None, stream=None):
+        """kvtc_mx_attn_shared: as attention, for sequences whose first
+        shared_pages pages are the first sequence's."""
+        return self._attention(batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream)
 
 
 def freq_tables(counts: torch.Tensor, alphabet: torch.Tensor, scale_bits: int):

@@ -1,0 +1,534 @@
+"""The microscaled paged cache on the GPU against the plain 64-bit
+implementation: writing and reading bit for bit, attention within bounds that
+follow from its roundings."""
+import numpy as np
+import pytest
+import torch
+
+import mx_ref
+from tensor_compression_amd import kvtc
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [(64, 4, 4), (64, 8, 4), (64, 4, 8), (64, 8, 8), (128, 4, 4), (128, 8, 4), (128, 4, 8), (128, 8, 8)]
+DT = {kvtc.BF16: torch.bfloat16, kvtc.FP32: torch.float32}
+
+
+def dev(x, dtype=None):
+    return torch.as_tensor(x, dtype=dtype).cuda()
+
+
+class Case:
+    """A cache, a batch of sequences (lens after their rows) in scattered pages."""
+
+    def __init__(self, D, bk, bv, dtype, H, rows, lens, layers=1, seed=0, fill=0xFF, shared=0, total_rows=None):
+        self.rng = np.random.default_rng(seed)
+        self.D, self.bk, self.bv, self.dtype, self.H, self.layers = D, bk, bv, dtype, H, layers
+        self.rows, self.lens = list(rows), list(lens)
+        self.starts = [0] + [int(x) for x in np.cumsum(rows)]
+        self.total = self.starts[-1] if total_rows is None else total_rows
+        need = [max(-(-x // 16), shared) for x in lens]
+        self.pages = shared + sum(x - shared for x in need) + 2
+        perm = [int(x) for x in self.rng.permutation(self.pages)]
+        at, self.table = shared, []
+        for x in need:
+            self.table.append(perm[:shared] + perm[at:at + x - shared])
+            at += x - shared
+        width = max(max(need, default=0), 1) + 1
+        # entries past a sequence's pages are outside the pool: nothing may follow them
+        self.table_dev = dev([t + [2 ** 30 + 5] * (width - len(t)) for t in self.table], torch.int32)
+        self.cache = kvtc.MxCache(dict(layers=layers, kv_heads=H, head_dim=D, dtype=dtype, bits_k=bk, bits_v=bv), self.pages)
+        self.cache.pool.fill_(fill)
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.batch = self.new_batch(rows, lens)
+
+    def new_batch(self, rows, lens, **kw):
+        starts = [0] + [int(x) for x in np.cumsum(rows)]
+        a = dict(total_rows=self.total, max_rows=max(rows), max_len=max(lens))
+        a.update(kw)
+        return self.cache.batch(self.table_dev, dev(list(lens), torch.int32), dev(starts, torch.int32), **a)
+
+    def rand(self, *shape, gain=0.6):
+        x = self.rng.standard_normal(shape) * np.exp(gain * self.rng.standard_normal(shape[-1]))
+        return dev(x, torch.float32).to(DT[self.dtype])
+
+    def fill(self):
+        """The whole sequences written by the library; returns the pool's bytes."""
+        t = sum(self.lens)
+        k, v = self.rand(t, self.H, self.D), self.rand(t, self.H, self.D)
+        b = self.cache.batch(self.table_dev, dev(self.lens, torch.int32),
+                             dev([0] + [int(x) for x in np.cumsum(self.lens)], torch.int32), total_rows=t,
+                             max_rows=max(self.lens), max_len=max(self.lens))
+        for layer in range(self.layers):
+            self.cache.write(b, k, v, layer=layer, status=self.status)
+        return self.cache.pool.cpu().numpy()
+
+    def unpacked(self, layer=0):
+        return mx_ref.unpack(self.cache.pool[layer].cpu().numpy(), self.D, self.bk, self.bv)
+
+
+def np64(x):
+    return x.double().cpu().numpy()
+
+
+# ---- writing and reading
+
+
+def hard_rows(rng, rows, H, D, dtype):
+    """Rows over the whole range of the type: blocks of every size, ties,
+    zeros of both signs, subnormals, the largest numbers, NaN and infinity."""
+    x = rng.standard_normal((rows, H, D)) * 2.0 ** rng.integers(-120, 120, (rows, H, D // 32, 1)).repeat(32, -1).reshape(rows, H, D)
+    flat = x.reshape(-1, 32)
+    m = len(flat)
+    flat[0 % m] = 0.0
+    flat[1 % m] = -0.0
+    flat[2 % m] = rng.integers(-14, 15, 32) / 4.0        # ties of both formats
+    flat[3 % m] = rng.integers(-1000, 1000, 32) / 2.0
+    flat[4 % m] = 2.0 ** -133 * rng.integers(-8, 8, 32)  # subnormals
+    flat[5 % m] = 3.38e38 * rng.uniform(-1, 1, 32)
+    flat[5 % m, 7] = 3.38e38
+    flat[6 % m, 3] = np.inf
+    flat[7 % m, 31] = -np.inf
+    flat[8 % m, 0] = np.nan
+    for i, lead in enumerate((1.75, 1.8125, 1.7421875, 1.8046875)):  # the scale's borders
+        flat[(9 + i) % m] = 0.25
+        flat[(9 + i) % m, 5] = lead * 2.0 ** (i - 2)
+    return dev(flat.reshape(rows, H, D), torch.float32).to(DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+@pytest.mark.parametrize("D,bk,bv", FORMATS)
+def test_write_bytes(D, bk, bv, dtype):
+    rows, lens = [1, 5, 16, 0, 17, 40, 3], [1, 5, 16, 7, 45, 40, 2]  # the last has a row before its first token
+    c = Case(D, bk, bv, dtype, 3, rows, lens, layers=2, seed=D + bk, fill=0xA5)
+    k, v = (hard_rows(c.rng, c.total, 3, D, dtype) for _ in range(2))
+    print("write", D, bk, bv, dtype, flush=True)
+    c.cache.write(c.batch, k, v, layer=1, status=c.status)
+    want = np.full(c.cache.pool.shape[1:], 0xA5, np.uint8)
+    mx_ref.write(want, c.table, lens, c.starts, np64(k), np64(v), D, bk, bv)
+    got = c.cache.pool.cpu().numpy()
+    assert np.array_equal(got[1], want)
+    assert (got[0] == 0xA5).all()
+    assert c.status.item() == 1 << kvtc.ERR_NONFINITE
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,bk,bv", FORMATS)
+def test_read_values(D, bk, bv, out):
+    rows, lens = [1, 5, 16, 0, 17, 33, 3], [1, 9, 16, 7, 45, 40, 2]
+    total = sum(rows) + 2
+    c = Case(D, bk, bv, kvtc.BF16, 3, rows, lens, layers=2, seed=D + bv, total_rows=total)
+    c.fill()
+    k = torch.full((total, 3, D), 7.0, dtype=out, device="cuda")
+    v = torch.full((total, 5, D), 7.0, dtype=out, device="cuda")[:, 1:4]  # a slice: strides of its own
+    print("read", D, bk, bv, out, flush=True)
+    c.cache.read(c.batch, k, v, layer=1, status=c.status)
+    for x, pages in ((k, c.unpacked(1)[0]), (v, c.unpacked(1)[1])):
+        want = np.full((total, 3, D), 7.0)
+        for z, ln in enumerate(lens):
+            for i in range(rows[z]):
+                pos = ln - rows[z] + i
+                if pos >= 0:
+                    want[c.starts[z] + i] = pages[c.table[z][pos // 16], :, pos % 16]
+        assert np.array_equal(np64(x), want)
+    assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_write_and_read_whole_cache(dtype):
+    """[L, H, T, D] in and out, through strides, in one call for all layers;
+    NaN blocks come back as NaN."""
+    D, L, H, T = 128, 3, 2, 77
+    c = Case(D, 8, 4, dtype, H, [T], [T], layers=L, seed=5)
+    k = c.rand(L, T, H, D).transpose(1, 2)  # layer, head and token strides out of order
+    v = c.rand(L, H, T, D)
+    v[1, 1, 3, 40] = float("nan")
+    c.cache.write(c.batch, k, v, status=c.status)
+    ko, vo = (torch.empty(L, H, T, D, dtype=DT[dtype], device="cuda") for _ in range(2))
+    c.cache.read(c.batch, ko, vo, status=c.status)
+    for x, y, b in ((k, ko, 8), (v, vo, 4)):
+        want = mx_ref.values(*mx_ref.quantise(np64(x), b), b)
+        assert np.array_equal(np64(y), want, equal_nan=True)
+    assert torch.isnan(vo[1, 1, 3, 32:64]).all() and not torch.isnan(vo[1, 1, 3, :32]).any()
+    assert c.status.item() == 1 << kvtc.ERR_NONFINITE
+    with pytest.raises(kvtc.KvtcError):
+        c.cache.read(c.batch, ko[:1].expand(L, H, T, D), vo)
+    with pytest.raises(ValueError):
+        c.cache.write(c.batch, k[:, :1], v)
+
+
+def test_appending_token_by_token_is_writing_at_once():
+    D, H = 64, 2
+    c = Case(D, 4, 8, kvtc.BF16, H, [37, 20], [37, 20], seed=6, fill=0)
+    k, v = c.rand(57, H, D), c.rand(57, H, D)
+    c.cache.write(c.batch, k, v)
+    want = c.cache.pool.clone()
+    c.cache.pool.zero_()
+    c.total = 2
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    starts = dev([0, 1, 2], torch.int32)
+    b = c.cache.batch(c.table_dev, lens, starts, total_rows=2, max_rows=1, max_len=37)
+    for t in range(37):
+        at = [t, 37 + min(t, 19)]
+        lens += dev([1, 1 if t < 20 else 0], torch.int32)
+        if t >= 20:
+            starts.copy_(dev([0, 1, 1], torch.int32))
+        c.cache.write(b, k[at], v[at])
+    assert torch.equal(c.cache.pool, want)
+
+
+# ---- attention
+
+
+def check_attention(c, q, got, lse, scale, causal, what):
+    """Bounds: bf16 weights and outputs are off by at most 2^-8 of themselves
+    each (fp32: the three-part weights and the output 2^-23), the scores by
+    D 2^-24 of the sum of their terms' magnitudes (exact products, fp32 sums)
+    and a few roundings of the exponent, the sums of T weights in 32-token
+    steps by T / 32 + 64 roundings of 2^-24."""
+    kp, vp = c.unpacked()
+    kp, vp = np.nan_to_num(kp), np.nan_to_num(vp)
+    want, wlse, mass, spread = mx_ref.attention(kp, vp, c.table, c.lens, c.starts, np64(q), scale, causal)
+    n = c.starts[-1]
+    o, s = np64(got)[:n], np64(lse)[:n]
+    u = 2.0 ** -8 if c.dtype == kvtc.BF16 else 2.0 ** -23
+    T = max(c.lens)
+    ew = spread * (c.D * 2.0 ** -24 + 4 * 2.0 ** -24) + 2.0 ** -21
+    steps = (T / 32 + 64) * 2.0 ** -24
+    tol = (u + 2 * ew[..., None] + 2 * steps) * mass + u * np.abs(want) + 1e-30
+    err = np.abs(o - want[:n])
+    worst = float((err / tol[:n]).max())
+    print(what, "worst error / bound %.3f" % worst, flush=True)
+    assert worst <= 1.0
+    empty = np.isneginf(wlse[:n])
+    assert np.array_equal(np.isneginf(s), empty) and not o[empty].any()
+    ltol = ew[:n] + steps + np.abs(np.where(empty, 0, wlse[:n])) * 2.0 ** -22
+    assert (np.abs(np.where(empty, 0, s) - np.where(empty, 0, wlse[:n])) <= ltol).all()
+
+
+def run_attention(c, G, causal=True, shared=None, scale=None, **kw):
+    q = c.rand(c.total, c.H * G, c.D, gain=0.2)
+    out = torch.full((c.total, c.H * G, c.D), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((c.total, c.H * G), 7.0, device="cuda")
+    scale = c.D ** -0.5 if scale is None else scale
+    if shared is None:
+        c.cache.attention(c.batch, q, scale, causal, out=out, lse=lse, status=c.status, **kw)
+    else:
+        c.cache.attention_shared(c.batch, q, shared, scale, causal, out=out, lse=lse, status=c.status, **kw)
+    assert c.status.item() == 0
+    n = c.starts[-1]
+    assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()
+    return q, out, lse, scale
+
+
+LENS = [1, 15, 16, 17, 31, 32, 33, 0, 5, 130, 257, 700]
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+@pytest.mark.parametrize("D,bk,bv", FORMATS)
+def test_attention_formats(D, bk, bv, dtype):
+    """Ragged lengths, sequences with no rows, no tokens, or more rows than
+    tokens, in a pool whose unwritten bytes are all NaN."""
+    rows = [1, 1, 2, 1, 3, 1, 5, 1, 7, 1, 0, 2]
+    c = Case(D, bk, bv, dtype, 2, rows, LENS, seed=D + bk + bv, total_rows=sum(rows) + 3)
+    c.fill()
+    q, out, lse, scale = run_attention(c, 3)
+    check_attention(c, q, out, lse, scale, True, f"D{D} k{bk} v{bv} dtype {dtype}")
+
+
+@pytest.mark.parametrize("G", [1, 2, 5, 8, 16, 24])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_groups(G, causal):
+    """Groups of 1 to 24 heads: tiles of 16, 32 and 64 rows, some part full."""
+    for dtype in (kvtc.BF16, kvtc.FP32):
+        rows = [1, 4, 2, 1]
+        c = Case(128, 4, 4, dtype, 3, rows, [40, 129, 2, 300], seed=G)
+        c.fill()
+        q, out, lse, scale = run_attention(c, G, causal)
+        check_attention(c, q, out, lse, scale, causal, f"G{G} causal {causal} dtype {dtype}")
+
+
+@pytest.mark.parametrize("D,bk,bv", [(64, 8, 8), (128, 4, 4), (128, 8, 4)])
+def test_attention_long_rows(D, bk, bv):
+    """Prompts: many rows a sequence, with and without tokens before them."""
+    for dtype in (kvtc.BF16, kvtc.FP32):
+        rows, lens = [200, 61, 90], [200, 333, 64]
+        c = Case(D, bk, bv, dtype, 2, rows, lens, seed=bk)
+        c.fill()
+        q, out, lse, scale = run_attention(c, 2)
+        check_attention(c, q, out, lse, scale, True, f"rows D{D} k{bk} v{bv} dtype {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_attention_long_context(dtype):
+    """One sequence over many ranges, lengths around their borders."""
+    for ln in (2047, 2049, 20011):
+        c = Case(128, 8, 4, dtype, 2, [2], [ln], seed=ln)
+        c.fill()
+        q, out, lse, scale = run_attention(c, 4)
+        check_attention(c, q, out, lse, scale, True, f"context {ln} dtype {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+@pytest.mark.parametrize("shared", [0, 1, 3, 40])
+def test_attention_shared_prefix(shared, dtype):
+    """Sequences past, at the end of, and inside the prefix, empty ones, and
+    sequences without rows; equal to the plain call on the same tables."""
+    p = 16 * shared
+    lens = [p + 1, p + 40, p, max(p - 5, 0), 0, p + 300, p + 16, min(p, 3)]
+    rows = [1, 2, 1, 3, 1, 0, 1, 1]
+    for D, bk, bv, G in ((128, 4, 4, 4), (64, 8, 4, 3)):
+        c = Case(D, bk, bv, dtype, 2, rows, lens, seed=shared + D, shared=shared, total_rows=sum(rows) + 1)
+        c.fill()
+        q, out, lse, scale = run_attention(c, G, shared=shared)
+        check_attention(c, q, out, lse, scale, True, f"shared {shared} D{D} dtype {dtype}")
+        # entries of the other sequences for the prefix are not read
+        out2 = torch.full_like(out, 7.0)
+        if shared:
+            c.table_dev[1:, :shared] = -1
+            c.cache.attention_shared(c.batch, q, shared, scale, out=out2, status=c.status)
+            assert torch.equal(out, out2) and c.status.item() == 0
+
+
+def test_attention_shared_prefix_many_rows():
+    """Enough rows together for whole 64-row tiles of the prefix pass."""
+    lens = [160 + int(x) for x in np.random.default_rng(1).integers(0, 90, 70)]
+    c = Case(128, 4, 4, kvtc.BF16, 2, [1 + z % 2 for z in range(70)], lens, seed=2, shared=10)
+    c.fill()
+    for causal in (True, False):
+        q, out, lse, scale = run_attention(c, 4, causal, shared=10)
+        check_attention(c, q, out, lse, scale, causal, f"shared rows causal {causal}")
+
+
+@pytest.mark.parametrize("scale", [1e-3, 1.0, 8.0])
+def test_attention_scales(scale):
+    """Flat and needle-sharp weights, scores that grow along the sequence."""
+    c = Case(64, 8, 8, kvtc.FP32, 1, [3], [500], seed=9)
+    c.fill()
+    q, out, lse, scale = run_attention(c, 4, scale=scale)
+    check_attention(c, q, out, lse, scale, True, f"scale {scale}")
+    t = c.lens[0]
+    k = torch.ones(t, 1, 64, device="cuda") * torch.linspace(-30, 30, t, device="cuda")[:, None, None]
+    b = c.new_batch([t], [t], total_rows=t)
+    c.cache.write(b, k, c.rand(t, 1, 64))
+    for sign in (1.0, -1.0):
+        q = torch.full((3, 4, 64), sign, device="cuda")
+        lse = torch.empty(3, 4, device="cuda")
+        out, _ = c.cache.attention(c.batch, q, scale, lse=lse)
+        check_attention(c, q, out, lse, scale, True, f"ramp {sign} scale {scale}")
+
+
+@pytest.mark.parametrize("D,bv", [(64, 4), (64, 8), (128, 4), (128, 8)])
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_nan_tokens_reach_only_rows_that_attend_to_them(D, bv, dtype):
+    rows, ln, H, G = 20, 100, 2, 2
+    for kv, pos in ((0, 90), (1, 90), (1, 99), (1, 81), (0, 99)):
+        c = Case(D, 8, bv, dtype, H, [rows], [ln], seed=pos)
+        k, v = c.rand(ln, H, D), c.rand(ln, H, D)
+        (k, v)[kv][pos, 1, 33] = float("nan")
+        b = c.new_batch([ln], [ln], total_rows=ln)
+        c.cache.write(b, k, v)
+        q = c.rand(rows, H * G, D)
+        out = c.cache.attention(c.batch, q)
+        want = torch.zeros(rows, H * G, D, dtype=torch.bool, device="cuda")
+        first = pos - (ln - rows)
+        want[first:, G:, :] = kv == 0
+        want[first:, G:, 32:64] = True
+        assert torch.equal(torch.isnan(out), want), (kv, pos)
+    # as a query: its own row and head only
+    q[3, 1, 5] = float("nan")
+    want = torch.isnan(out)
+    out2 = c.cache.attention(c.batch, q)
+    want[3, 1] = True
+    assert torch.equal(torch.isnan(out2), want)
+
+
+def test_nan_tokens_in_the_prefix_pass():
+    """A sequence inside the prefix does not see the NaN that the others see."""
+    c = Case(128, 4, 4, kvtc.BF16, 1, [1, 1, 1], [32, 20, 40], shared=2, seed=4)
+    k, v = c.rand(92, 1, 128), c.rand(92, 1, 128)
+    k[32:52], v[32:52] = k[:20], v[:20]
+    k[52:84], v[52:84] = k[:32], v[:32]
+    for x in (0, 52):
+        v[x + 25, 0, 100] = float("nan")
+    b = c.cache.batch(c.table_dev, dev(c.lens, torch.int32), dev([0, 32, 52, 92], torch.int32), total_rows=92,
+                      max_rows=40, max_len=40)
+    c.cache.write(b, k, v)
+    q = c.rand(3, 2, 128)
+    nan = torch.isnan(c.cache.attention_shared(c.batch, q, 2))
+    want = torch.zeros_like(nan)
+    want[0, :, 96:] = True
+    want[2, :, 96:] = True
+    assert torch.equal(nan, want)
+
+
+def test_attention_infinite_query():
+    """An infinite query spoils its own row and head, nothing else."""
+    c = Case(64, 8, 4, kvtc.BF16, 1, [4], [60], seed=12)
+    c.fill()
+    q = c.rand(4, 2, 64)
+    good = c.cache.attention(c.batch, q)
+    q[1, 0, 3] = float("inf")
+    out = c.cache.attention(c.batch, q)
+    keep = torch.ones(4, 2, dtype=torch.bool, device="cuda")
+    keep[1, 0] = False
+    assert torch.equal(out[keep], good[keep])
+
+
+# ---- metadata that is wrong, streams, graphs
+
+
+def test_bad_metadata_is_reported_and_skipped():
+    bad_bit = 1 << kvtc.ERR_INVALID_ARG
+    H, D = 2, 128
+
+    def fresh():
+        c = Case(D, 4, 4, kvtc.BF16, H, [2, 3, 1], [40, 20, 33], seed=8)
+        c.fill()
+        q = c.rand(6, H * 2, D)
+        return c, q, c.cache.attention(c.batch, q)
+
+    # lengths outside the bounds, row ranges outside the tensors or backwards
+    for lens, starts in (([40, 41, 33], [0, 2, 5, 6]), ([40, -1, 33], [0, 2, 5, 6]), ([40, 20, 33], [0, 2, 6, 7]),
+                         ([40, 20, 33], [0, 5, 2, 3]), ([40, 20, 33], [0, 2, 6, 6])):
+        c, q, good = fresh()
+        b = c.cache.batch(c.table_dev, dev(lens, torch.int32), dev(starts, torch.int32), total_rows=6, max_rows=3, max_len=40)
+        out = torch.full_like(q, 7.0)
+        print("bad metadata", lens, starts, flush=True)
+        c.cache.attention(b, q, out=out, status=c.status)
+        assert c.status.item() == bad_bit
+        if starts[1] == 2:
+            assert torch.equal(out[:2], good[:2])
+        before = c.cache.pool.clone()
+        c.status.zero_()
+        c.cache.write(b, c.rand(6, H, D), c.rand(6, H, D), status=c.status)
+        assert c.status.item() == bad_bit
+        for z in range(3):
+            n = starts[z + 1] - starts[z]
+            if not (0 <= lens[z] <= 40 and 0 <= n <= 3 and starts[z + 1] <= 6 and starts[z] >= 0):
+                assert torch.equal(c.cache.pool[0, c.table[z]], before[0, c.table[z]])
+        c.status.zero_()
+        c.cache.read(b, torch.empty(6, H, D, device="cuda"), torch.empty(6, H, D, device="cuda"), status=c.status)
+        assert c.status.item() == bad_bit
+    # pages outside the pool: their tokens are masked, everything else as without them
+    for page in (-1, 2 ** 31 - 1, "pages"):
+        c, q, good = fresh()
+        page = c.pages if page == "pages" else page
+        c.table_dev[1, 1] = page
+        out = torch.full_like(q, 7.0)
+        print("bad page", page, flush=True)
+        c.cache.attention(c.batch, q, out=out, status=c.status)
+        assert c.status.item() == bad_bit and torch.equal(out[:2], good[:2]) and torch.equal(out[5:], good[5:])
+        kp, vp = c.unpacked()
+        want, _, _, _ = mx_ref.attention(kp, vp, [c.table[1]], [16], [0, 1], np64(q)[4:5], D ** -0.5, True)
+        assert np.abs(np64(out[4:5]) - want).max() < 0.05
+        before = c.cache.pool.clone()
+        c.cache.write(c.batch, c.rand(6, H, D), c.rand(6, H, D), status=c.status)
+        assert torch.equal(c.cache.pool[0, c.table[1]], before[0, c.table[1]])
+        k = torch.full((6, H, D), 7.0, device="cuda")
+        c.cache.read(c.batch, k, k.clone(), status=c.status)
+        assert (k[2:5] == 7.0).all() and not (k[:2] == 7.0).any()
+    # a call that is fine adds nothing
+    c, q, good = fresh()
+    c.cache.attention(c.batch, q, status=c.status)
+    assert c.status.item() == 0
+
+
+def test_repeatable_and_on_other_streams():
+    c = Case(128, 4, 8, kvtc.BF16, 2, [1] * 6, [900, 3, 77, 2000, 512, 1], seed=13)
+    c.fill()
+    q = c.rand(6, 8, 128)
+    good = c.cache.attention(c.batch, q)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(3):
+        for s in streams:  # both at once, each with a workspace of its own
+            outs.append(c.cache.attention(c.batch, q, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, good) for o in outs)
+
+
+def test_captured_calls_follow_the_device_arrays():
+    """A step (write, attend, shared prefix) captured once and replayed while
+    lengths, pages and rows change; every replay against the eager call."""
+    D, H, G, n = 128, 2, 4, 3
+    c = Case(D, 8, 4, kvtc.BF16, H, [1] * n, [300, 300, 300], seed=14, shared=2)
+    c.fill()
+    lens, starts = dev([33, 40, 35], torch.int32), dev([0, 1, 2, 3], torch.int32)
+    b = c.cache.batch(c.table_dev, lens, starts, total_rows=n, max_rows=1, max_len=300)
+    k, v, q = c.rand(n, H, D), c.rand(n, H, D), c.rand(n, H * G, D)
+    out, out2 = torch.empty_like(q), torch.empty_like(q)
+    ws, ws2 = c.cache.workspace(b, H * G), c.cache.workspace(b, H * G, 2)
+
+    def step(o, o2):
+        c.cache.write(b, k, v, status=c.status)
+        c.cache.attention(b, q, out=o, ws=ws, status=c.status)
+        c.cache.attention_shared(b, q, 2, out=o2, ws=ws2, status=c.status)
+
+    step(out, out2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(out, out2)
+    for r in range(6):
+        lens.copy_(dev([33 + 40 * r, 40 + 3 * r, 35 + 50 * r], torch.int32))
+        q.copy_(c.rand(n, H * G, D))
+        k.copy_(c.rand(n, H, D))
+        if r == 3:
+            c.table_dev[0, 5], c.table_dev[1, 5] = int(c.table[1][5]), int(c.table[0][5])
+        g.replay()
+        torch.cuda.synchronize()
+        pool = c.cache.pool.clone()
+        e, e2 = torch.empty_like(q), torch.empty_like(q)
+        step(e, e2)
+        assert torch.equal(pool, c.cache.pool) and torch.equal(out, e) and torch.equal(out2, e2), r
+    assert c.status.item() == 0
+
+
+def test_decoded_cache_is_served_and_encoded_again():
+    """As a serving program uses the two together: a container is decoded, its
+    cache goes into pages, a conversation goes on for some steps (fused
+    projections, one layer after the other), and the grown cache is read back
+    and encoded."""
+    L, H, G, D, T = 2, 2, 4, 128, 300
+    cfg = dict(layers=L, kv_heads=H, head_dim=D, dtype=kvtc.BF16, transform=kvtc.PCA, sink_tokens=4, recent_tokens=32,
+               bits_k=4.0, bits_v=4.0, max_bits=8, rope_keys=0, rope_style=0, rope_theta=10000.0, rans_scale_bits=12,
+               rans_lanes=32, chunk_tokens=1024, tile_tokens=128, basis_per_head=0, wht_keys=0)
+    basis = torch.eye(D).expand(L, 2, D, D).contiguous()
+    plan = kvtc.Plan(cfg, basis, max_tokens=400)
+    c = Case(D, 8, 4, kvtc.BF16, H, [T], [T], layers=L, seed=15)
+    data, st = plan.encode(c.rand(L, H, T, D), c.rand(L, H, T, D))
+    assert st == kvtc.OK
+    K, V, st = plan.decode(data, T, kvtc.BF16)
+    assert st == kvtc.OK
+    total = T + 10
+    table = dev([list(range(-(-total // 16)))], torch.int32)
+    cache = kvtc.MxCache(dict(layers=L, kv_heads=H, head_dim=D, dtype=kvtc.BF16, bits_k=8, bits_v=4), table.shape[1])
+    lens = dev([T], torch.int32)
+    cache.write(cache.batch(table, lens, dev([0, T], torch.int32), T, T, total), K, V, status=c.status)
+    rows_k, rows_v = [np64(K)], [np64(V)]
+    step = cache.batch(table, lens, dev([0, 1], torch.int32), total_rows=1, max_rows=1, max_len=total)
+    for t in range(T, total):
+        lens += 1
+        new = []
+        for layer in range(L):
+            qkv = c.rand(1, (G + 2) * H, D)
+            q, k, v = qkv.split([G * H, H, H], 1)
+            cache.write(step, k, v, layer=layer, status=c.status)
+            out = cache.attention(step, q, layer=layer, status=c.status)
+            new.append((np64(k)[0], np64(v)[0]))
+            kp, vp = mx_ref.unpack(cache.pool[layer].cpu().numpy(), D, 8, 4)
+            want, _, mass, _ = mx_ref.attention(kp, vp, [list(range(table.shape[1]))], [t + 1], [0, 1], np64(q), D ** -0.5, True)
+            assert (np.abs(np64(out) - want) <= 2.0 ** -7 * mass + 2.0 ** -8 * np.abs(want)).all()
+        rows_k.append(np.stack([x[0] for x in new])[:, :, None])
+        rows_v.append(np.stack([x[1] for x in new])[:, :, None])
+    ko, vo = (torch.empty(L, H, total, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cache.read(cache.batch(table, lens, dev([0, total], torch.int32), total, total, total), ko, vo, status=c.status)
+    for got, rows, b in ((ko, rows_k, 8), (vo, rows_v, 4)):
+        want = mx_ref.values(*mx_ref.quantise(np.concatenate(rows, 2), b), b)
+        assert np.array_equal(np64(got), want)
+    data, st = plan.encode(ko, vo)
+    assert st == kvtc.OK and c.status.item() == 0
+    k2, v2, st = plan.decode(data, total, kvtc.BF16)
+    assert st == kvtc.OK and torch.equal(k2[:, :, -32:], ko[:, :, -32:])
