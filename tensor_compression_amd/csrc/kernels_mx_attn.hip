@@ -68,12 +68,6 @@ __device__ __forceinline__ float rest(float x, uint32_t h, int hi) {
   return x - __uint_as_float(hi ? h & 0xFFFF0000u : h << 16);
 }
 
-// A lane's share of one page as it lies in the record.
-template <int KW, int VW>
-struct Page {
-  uint32_t k[KW], v[VW], ks, vs;
-};
-
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[N]) {
   if constexpr (N == 2) {
@@ -114,354 +108,432 @@ __device__ __forceinline__ int limit_of(const MxSeq& s, int i, int causal) {
   return causal ? max(s.len - s.n + i + 1, 0) : s.len;
 }
 
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = min(v, __shfl_xor(v, o));
-  return v;
+// Least and greatest value of a 16-lane row.
+__device__ __forceinline__ int row_min(int v) {
+  v = min(v, (int)xor16_u32<1>((uint32_t)v));
+  v = min(v, (int)xor16_u32<2>((uint32_t)v));
+  v = min(v, (int)xor16_u32<4>((uint32_t)v));
+  return min(v, (int)xor16_u32<8>((uint32_t)v));
 }
-__device__ __forceinline__ int wave_max(int v) {
+__device__ __forceinline__ int row_max(int v) { return -row_min(-v); }
+
+// The 16 NT query rows from r0 on, column n of each tile in lane n: tensor
+// row (-1 for none), query head, tokens it attends to.  lo, hi: every row
+// attends to the tokens below lo, none to those from hi on.
+template <int NT>
+struct Rows {
+  int at[NT], head[NT], lim[NT], lo, hi;
+};
+template <int NT>
+__device__ __forceinline__ Rows<NT> rows_of(const MxAttnParams& p, const MxSeq& sq, int h, int r0, int rows, int n) {
+  Rows<NT> o;
+  o.lo = 0x7FFFFFFF;
+  o.hi = 0;
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = max(v, __shfl_xor(v, o));
-  return v;
+  for (int t = 0; t < NT; ++t) {
+    const int r = r0 + 16 * t + n, i = r / p.G;
+    o.at[t] = -1;
+    o.head[t] = h * p.G + r - i * p.G;
+    o.lim[t] = 0;
+    if (r < rows) {
+      if (p.prefix) {
+        const MxSeq s = mx_seq(p.b, seq_of(p.b, i), p.status);
+        if (i >= s.row0 && i < s.row0 + s.n) {
+          o.at[t] = i;
+          o.lim[t] = limit_of(s, i - s.row0, p.causal);
+        }
+      } else {
+        o.at[t] = sq.row0 + i;
+        o.lim[t] = limit_of(sq, i, p.causal);
+      }
+    }
+    if (o.at[t] >= 0) o.lo = min(o.lo, o.lim[t]);
+    o.hi = max(o.hi, o.lim[t]);
+  }
+  o.lo = __builtin_amdgcn_readfirstlane(row_min(o.lo));
+  o.hi = __builtin_amdgcn_readfirstlane(row_max(o.hi));
+  return o;
 }
 
+// Query operands: channels (D / 4) kg + 8 s .. + 7 of the lane's row, as bf16
+// or as three bf16 parts.
+template <int D, int NT, bool F32>
+__device__ __forceinline__ void load_queries(const MxAttnParams& p, const Rows<NT>& rw, int kg,
+                                             bf16x8_t (&q)[NT][D / 32][F32 ? 3 : 1]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t off = rw.at[t] * p.q_stride + rw.head[t] * D + (D / 4) * kg;
+#pragma unroll
+    for (int s = 0; s < D / 32; ++s) {
+      if constexpr (!F32) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (rw.at[t] >= 0) w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + off + 8 * s);
+        q[t][s][0] = __builtin_bit_cast(bf16x8_t, w);
+      } else {
+        float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (rw.at[t] >= 0) {
+          const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + off + 8 * s);
+          x[0] = src[0];
+          x[1] = src[1];
+        }
+        float f[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          uint32_t u[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            u[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+            f[2 * i] = rest(f[2 * i], u[i], 0);
+            f[2 * i + 1] = rest(f[2 * i + 1], u[i], 1);
+          }
+          q[t][s][k] = operand(u[0], u[1], u[2], u[3]);
+        }
+      }
+    }
+  }
+}
+
+// Where a lane finds its share of a record.
+template <int D, int BK, int BV>
+struct Share {
+  static constexpr MxRecord R = mx_record(D, BK, BV);
+  static constexpr int KW = D * BK / 128, VW = D * BV / 128;  // words of keys and values
+  int k, v, ks, vs;
+  __device__ __forceinline__ Share(int n, int kg)
+      : k(n * (D * BK / 8) + kg * KW * 4),
+        v(R.kc + (kg * 16 + n) * VW * 4),
+        ks(R.kc + R.vc + n * (D / 32) + kg * (D / 32) / 4),
+        vs(R.kc + R.vc + R.sc + (kg * (D / 32) + n * (D / 16) / 32) * 4) {}
+};
+
+// Value words of a lane: token i of its four without value, scale 1.
+template <int VW>
+__device__ __forceinline__ void drop(uint32_t (&v)[VW], uint32_t& vs, int i) {
+  if constexpr (VW == 2) v[i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+  else {
+#pragma unroll
+    for (int w = 0; w < VW / 4; ++w) v[i * (VW / 4) + w] = 0;
+  }
+  vs = (vs & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
+}
+__device__ __forceinline__ bool nan_scale(uint32_t vs, int i) { return ((vs >> (8 * i)) & 0xFFu) == 0xFFu; }
+
+// Channel pair c2 of the lane's entry at its four tokens, a word per channel
+// and token pair: even channel in x[0], x[1], odd channel in x[2], x[3].
+template <int D, int BV, int c2, int VW>
+__device__ __forceinline__ void value_words(const uint32_t (&v)[VW], uint32_t vs, uint32_t (&x)[4]) {
+  constexpr int C = D / 16;
+  uint32_t y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float sc = __uint_as_float(((vs >> (8 * i)) & 0xFFu) << 23);
+    if constexpr (BV == 4 && C == 8) y[i] = two<4, c2>(v[i], sc);
+    else if constexpr (BV == 4) y[i] = (i & 1) ? two<4, 2 + c2>(v[i / 2], sc) : two<4, c2>(v[i / 2], sc);
+    else y[i] = two<8, c2 & 1>(v[i * (C / 4) + c2 / 2], sc);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[i] = __builtin_amdgcn_perm(y[2 * i + 1], y[2 * i], 0x05040100u);
+    x[2 + i] = __builtin_amdgcn_perm(y[2 * i + 1], y[2 * i], 0x07060302u);
+  }
+}
+
+// Rows of a score tile that attend to a NaN value: bit 4 t + b for channel
+// block b.  vs: the value scales of the lane's four tokens of a page.
+template <int D, int NT>
+__device__ __forceinline__ void mark_poison(const uint8_t* vs, int t0, int have, const int (&lim)[NT], uint32_t& poison) {
+  for (int i = 0; i < 4; ++i)
+    if (i < have)
+      for (int b = 0; b < D / 32; ++b)
+        if (vs[4 * b + i] == 0xFFu) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (t0 + i < lim[t]) poison |= 1u << (4 * t + b);
+        }
+}
+
+// Running softmax of NT tiles over a pair of pages: scores in, weights out as
+// PV operands.  One vote decides whether any maximum has to move.
+template <int NT, int C, int NP>
+struct Softmax {
+  float m[NT], l[NT], raise[NT];  // raise: the score from which on the maximum moves
+  __device__ __forceinline__ Softmax() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t] = raise[t] = kLow;
+      l[t] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void step(const f32x4_t (&s)[NT][2], float c, float inv_c, f32x4_t (&acc)[NT][C],
+                                       bf16x8_t (&pf)[NT][NP]) {
+    float mx[NT];
+    bool up = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      mx[t] = fmaxf(fmaxf(fmaxf(s[t][0][0], s[t][0][1]), fmaxf(s[t][0][2], s[t][0][3])),
+                    fmaxf(fmaxf(s[t][1][0], s[t][1][1]), fmaxf(s[t][1][2], s[t][1][3])));
+      up |= mx[t] > raise[t];
+    }
+    if (__builtin_amdgcn_ballot_w64(up)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float x = mx[t] * c;
+        x = fmaxf(x, __shfl_xor(x, 16));
+        x = fmaxf(x, __shfl_xor(x, 32));
+        const float nm = fmaxf(m[t], x), a = __builtin_amdgcn_exp2f(m[t] - nm);
+        m[t] = nm;
+        raise[t] = (nm + kSlack) * inv_c;
+        l[t] *= a;
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[t][j] *= a;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __builtin_amdgcn_exp2f(__fmaf_rn(s[t][i / 4][i % 4], c, -m[t]));
+      l[t] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
+          if (k + 1 < NP) {
+            w[2 * i] = rest(w[2 * i], x[i], 0);
+            w[2 * i + 1] = rest(w[2 * i + 1], x[i], 1);
+          }
+        }
+        pf[t][k] = operand(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+};
+
+// Scores of tokens that a row does not attend to: `top` of the lane's four
+// tokens of a page count.
+__device__ __forceinline__ void mask(f32x4_t& s, int top) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = i < top ? s[i] : -INFINITY;
+}
+
+// A row's result: the partial sums, or o / L and the log-sum-exp.
+template <bool F32, int N>
+__device__ __forceinline__ void store_row(float* ws_o, void* out, int64_t at, int D, int c0, const float (&o)[N], float L) {
+  if (ws_o) {
+    float4* d = reinterpret_cast<float4*>(ws_o + at * D + c0);
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) d[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    return;
+  }
+  const float r = L == 0.f ? 0.f : 1.0f / L;
+  if constexpr (F32) {
+    float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + at * D + c0);
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) d[j] = make_float4(o[4 * j] * r, o[4 * j + 1] * r, o[4 * j + 2] * r, o[4 * j + 3] * r);
+  } else {
+    uint2* d = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + at * D + c0);
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j)
+      d[j] = make_uint2(pack_bf16(o[4 * j] * r, o[4 * j + 1] * r), pack_bf16(o[4 * j + 2] * r, o[4 * j + 3] * r));
+  }
+}
+__device__ __forceinline__ float log_sum(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+// What a workgroup works on.  Heads vary fastest, so that (with 8 of them) a
+// head's tiles stay on one XCD and its pages in one L2; the last tiles,
+// longest when causal, come first.
+struct Work {
+  int h, tile, split, z;
+};
+__device__ __forceinline__ Work work_of(const MxAttnParams& p) {
+  Work w;
+  int b = blockIdx.x;
+  w.h = b % p.H;
+  b /= p.H;
+  w.tile = p.tiles - 1 - b % p.tiles;
+  b /= p.tiles;
+  w.split = b % p.nsplit;
+  w.z = b / p.nsplit;
+  return w;
+}
+
+// Few rows: memory bound, one pass over the codes with as many loads in
+// flight as the registers allow.  The waves take pairs of pages in turn, all
+// for the same 16 NT rows, and are joined at the end.
 template <int D, int BK, int BV, int NT, bool F32>
-__global__ __launch_bounds__(256, 2) void k_mx_attn(const MxAttnParams p) {
-  constexpr MxRecord R = mx_record(D, BK, BV);
-  constexpr int C = D / 16;                            // channels of an entry of the value groups
-  constexpr int KS = D / 32;                           // contraction steps of S
-  constexpr int KW = D * BK / 128, VW = D * BV / 128;  // words of a lane's share of a page
-  constexpr int NP = F32 ? 3 : 1;                      // bf16 parts of queries and weights
-  constexpr bool QL = NT > 2 || F32;                   // queries in LDS
-  constexpr int OS = D + 4;                            // row stride of the joining buffer
+__global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const MxAttnParams p) {
+  using Sh = Share<D, BK, BV>;
+  constexpr MxRecord R = Sh::R;
+  constexpr int C = D / 16;       // channels of an entry of the value groups
+  constexpr int KS = D / 32;      // contraction steps of S
+  constexpr int NP = F32 ? 3 : 1;  // bf16 parts of queries and weights
+  constexpr int OS = D + 4;       // row stride of the joining buffer
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, kg = lane >> 4;
-
-  // heads vary fastest, so that (with 8 of them) a head's tiles stay on one
-  // XCD and its pages in one L2; the last tiles, longest when causal, first
-  int bid = blockIdx.x;
-  const int h = bid % p.H;
-  bid /= p.H;
-  const int tile = p.tiles - 1 - bid % p.tiles;
-  bid /= p.tiles;
-  const int split = bid % p.nsplit, z = bid / p.nsplit;
+  const Work wk = work_of(p);
+  const int h = wk.h;
 
   __shared__ __attribute__((aligned(16))) float lds[4 * 16 * OS];
   __shared__ float2 ml[4][16];
-  __shared__ int2 rowq[NT * 16];  // row and query head, row -1 for none
-  static_assert(!QL || NT * KS * NP * 1024 <= 4 * 16 * OS * 4, "the queries fit where the joining buffer is");
 
   const int Hq = p.H * p.G;
   MxSeq sq{0, 0, 0};
-  int rows;
-  if (p.prefix) rows = p.b.total_rows * p.G;
-  else {
-    sq = mx_seq(p.b, z, p.status);
-    rows = sq.n * p.G;
-  }
-  const int r0 = tile * 16 * NT;
+  if (!p.prefix) sq = mx_seq(p.b, wk.z, p.status);
+  const int rows = (p.prefix ? p.b.total_rows : sq.n) * p.G;
+  const int r0 = wk.tile * 16 * NT;
   if (r0 >= rows) return;
-
-  // ---- the rows of this lane's query column
-  int lim[NT], lo = 0x7FFFFFFF, hi = 0;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = r0 + 16 * t + n;
-    lim[t] = 0;
-    int at = -1;
-    if (r < rows) {
-      const int i = r / p.G;
-      int row = i;
-      bool ok = true;
-      if (p.prefix) {
-        const MxSeq s = mx_seq(p.b, seq_of(p.b, row), p.status);
-        ok = row >= s.row0 && row < s.row0 + s.n;
-        if (ok) lim[t] = limit_of(s, row - s.row0, p.causal);
-      } else {
-        row = sq.row0 + i;
-        lim[t] = limit_of(sq, i, p.causal);
-      }
-      if (ok) at = row;
-    }
-    if (at >= 0) lo = min(lo, lim[t]);
-    hi = max(hi, lim[t]);
-    if (wave == 0 && kg == 0) rowq[16 * t + n] = make_int2(at, h * p.G + r % p.G);
-  }
-  lo = __builtin_amdgcn_readfirstlane(wave_min(lo));  // every row attends to the tokens below
-  hi = __builtin_amdgcn_readfirstlane(wave_max(hi));  // and none from here on
-  const int begin = p.begin + split * p.chunk;
-  const int end = min(min(p.end, begin + p.chunk), hi);
+  const Rows<NT> rw = rows_of<NT>(p, sq, h, r0, rows, n);
+  const int begin = p.begin + wk.split * p.chunk;
+  const int end = min(min(p.end, begin + p.chunk), rw.hi);
   if (p.ws_o && begin >= end) return;
-  __syncthreads();  // rowq
 
-  // ---- queries: B operands, channels (D / 4) kg + 8 s .. + 7 of row n
-  bf16x8_t qf[QL ? 1 : NT][QL ? 1 : KS];
-  uint4* const ql = reinterpret_cast<uint4*>(lds);
-  if constexpr (QL) {
-    for (int f = wave; f < NT * KS; f += 4) {
-      const int t = f / KS, s = f % KS;
-      const int2 at = rowq[16 * t + n];
-      uint4 w[NP];
-#pragma unroll
-      for (int k = 0; k < NP; ++k) w[k] = make_uint4(0, 0, 0, 0);
-      if (at.x >= 0) {
-        const int64_t off = at.x * p.q_stride + at.y * D + (D / 4) * kg + 8 * s;
-        if constexpr (!F32) w[0] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + off);
-        else {
-          float x[8];
-          *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + off);
-          *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + off + 4);
-#pragma unroll
-          for (int k = 0; k < NP; ++k) {
-            uint32_t u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              u[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-              x[2 * i] = rest(x[2 * i], u[i], 0);
-              x[2 * i + 1] = rest(x[2 * i + 1], u[i], 1);
-            }
-            w[k] = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < NP; ++k) ql[(f * NP + k) * 64 + lane] = w[k];
-    }
-    __syncthreads();
-  } else {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int2 at = rowq[16 * t + n];
-      const int64_t off = at.x * p.q_stride + at.y * D + (D / 4) * kg;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (at.x >= 0) w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + off + 8 * s);
-        qf[t][s] = __builtin_bit_cast(bf16x8_t, w);
-      }
-    }
-  }
-
-  // ---- the pass over the tokens
-  f32x4_t acc[NT][C];
-  float m[NT], l[NT];
-  uint32_t poison[NT];  // channel blocks whose value was NaN at a token that the row attends to
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    m[t] = kLow;
-    l[t] = 0.f;
-    poison[t] = 0;
-#pragma unroll
-    for (int j = 0; j < C; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  }
-
-  const int32_t* table = p.b.page_table + (p.prefix ? 0 : (int64_t)z * p.b.max_pages);
+  const int32_t* table = p.b.page_table + (p.prefix ? 0 : (int64_t)wk.z * p.b.max_pages);
   const uint8_t* head = p.pool + (int64_t)h * R.bytes;
   const int64_t page_bytes = (int64_t)p.H * R.bytes;
-  const int k_off = n * (D * BK / 8) + kg * KW * 4;
-  const int v_off = R.kc + (kg * 16 + n) * VW * 4;
-  const int ks_off = R.kc + R.vc + n * (D / 32) + kg * (D / 32) / 4;
-  const int vs_off = R.kc + R.vc + R.sc + (kg * (D / 32) + n * C / 32) * 4;
-  const int p0 = begin / KVTC_MX_PAGE, p1 = (end + KVTC_MX_PAGE - 1) / KVTC_MX_PAGE;  // pages of the range
+  const Sh sh(n, kg);
+  const int p1 = (end + KVTC_MX_PAGE - 1) / KVTC_MX_PAGE;  // end of the range's pages
+  const int q0 = begin / KVTC_MX_PAGE + 2 * wave;          // this wave takes pages q0 + 8 k and q0 + 8 k + 1
+  const int steps = (p1 - q0 + 7) >> 3;
 
-  using PageT = Page<KW, VW>;
-  // pages past the range and pages outside the pool are read as page 0 and masked
-  auto page_id = [&](int pg) {
-    int id = pg < p1 ? table[pg] : -1;
-    id = __builtin_amdgcn_readfirstlane(id);
-    if (pg < p1 && (uint32_t)id >= (uint32_t)p.pool_pages) {
-      if (p.status && lane == 0) atomicOr(p.status, 1u << KVTC_ERR_INVALID_ARG);
-      id = -1;
+  // Page numbers: those of 32 steps at a time, one a lane, the next 32 steps'
+  // on their way; -1 past the range and, once reported, outside the pool
+  // (such pages are read as page 0 and masked).
+  auto load_ids = [&](int step) {
+    const int pg = q0 + (step + (lane >> 1)) * 8 + (lane & 1);
+    int id = -1;
+    if (pg < p1) {
+      id = table[pg];
+      if ((uint32_t)id >= (uint32_t)p.pool_pages) {
+        if (p.status) atomicOr(p.status, 1u << KVTC_ERR_INVALID_ARG);
+        id = -1;
+      }
     }
     return id;
   };
-  auto load_page = [&](int id, PageT& g) {
-    const uint8_t* rec = head + (int64_t)max(id, 0) * page_bytes;
-    load_words(rec + k_off, g.k);
-    load_words(rec + v_off, g.v);
-    g.ks = rec[ks_off];
-    g.vs = *reinterpret_cast<const uint32_t*>(rec + vs_off);
+  // A lane's share of a step's two pages as it lies in their records.  The
+  // keys of the next step are requested as soon as this step's have become
+  // operands, its values at the end of this step.
+  int id[2];
+  uint32_t k[2][Sh::KW], v[2][Sh::VW], ks[2], vs[2];
+  int ids = load_ids(0), ids2 = load_ids(32);
+  auto load_keys = [&](int step, bool later) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      id[e] = __builtin_amdgcn_readlane(later ? ids2 : ids, 2 * (step & 31) + e);
+      const uint8_t* rec = head + max(id[e], 0) * page_bytes;
+      load_words(rec + sh.k, k[e]);
+      ks[e] = rec[sh.ks];
+    }
+  };
+  auto load_values = [&]() {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint8_t* rec = head + max(id[e], 0) * page_bytes;
+      load_words(rec + sh.v, v[e]);
+      vs[e] = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
+    }
   };
 
-  int pg = p0 + 2 * wave;
-  int id[2], nid[2];
-  PageT g[2], ng[2];
-  if (pg < p1) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      nid[e] = page_id(pg + e);
-      load_page(nid[e], ng[e]);
-    }
+  bf16x8_t qf[NT][KS][NP];
+  load_queries<D, NT, F32>(p, rw, kg, qf);
+  if (steps > 0) {
+    load_keys(0, false);
+    load_values();
   }
-  for (; pg < p1; pg += 8) {
+
+  f32x4_t acc[NT][C];
+  Softmax<NT, C, NP> sm;
+  const float inv_c = 1.0f / p.c;
+  uint32_t poison = 0;  // bit 4 t + b: a value of channel block b was NaN at a token that row t attends to
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      id[e] = nid[e];
-      g[e] = ng[e];
-    }
-    if (pg + 8 < p1) {
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        nid[e] = page_id(pg + 8 + e);
-        load_page(nid[e], ng[e]);
-      }
+    for (int j = 0; j < C; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  for (int step = 0; step < steps; ++step) {
+    if (step && (step & 31) == 0) {
+      ids = ids2;
+      ids2 = load_ids(step + 32);
     }
-    const int t0 = pg * KVTC_MX_PAGE;
+    const int t0 = (q0 + 8 * step) * KVTC_MX_PAGE;
+    const bool more = step + 1 < steps;
     // tokens of page e that exist for this workgroup, 0 .. 16
     int have[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) have[e] = id[e] < 0 ? 0 : min(max(end - t0 - 16 * e, 0), 16);
-    const bool whole = have[0] + have[1] == 32 && t0 + 32 <= lo;
+    const bool whole = have[0] + have[1] == 32 && t0 + 32 <= rw.lo;
 
     if (!whole) {
-      // tokens that no row attends to may be anything: make their values 0
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * kg + i >= have[e]) {
-#pragma unroll
-            for (int w = 0; w < VW / 4 + (VW < 4); ++w) {
-              if constexpr (VW >= 4) g[e].v[i * (VW / 4) + w] = 0;
-              else g[e].v[i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-            }
-            g[e].vs = (g[e].vs & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
-          }
-      // a NaN value that only some rows attend to: 0 in the product, and a
-      // mark for the rows that do
+      // Values of tokens that no row attends to may be anything: make them 0.
+      // A NaN value that only some rows attend to: 0 in the product, and a
+      // mark for the rows that do.
       bool nan = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) nan |= ((g[e].vs >> (8 * i)) & 0xFFu) == 0xFFu;
+        for (int i = 0; i < 4; ++i) {
+          if (4 * kg + i >= have[e]) drop(v[e], vs[e], i);
+          nan |= nan_scale(vs[e], i);
+        }
       if (__builtin_amdgcn_ballot_w64(nan)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint8_t* vs = head + (int64_t)max(id[e], 0) * page_bytes + R.kc + R.vc + R.sc + kg * (D / 32) * 4;
+          mark_poison<D, NT>(head + max(id[e], 0) * page_bytes + R.kc + R.vc + R.sc + kg * (D / 32) * 4,
+                             t0 + 16 * e + 4 * kg, have[e] - 4 * kg, rw.lim, poison);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (4 * kg + i < have[e]) {
-#pragma unroll
-              for (int b = 0; b < D / 32; ++b)
-                if (vs[4 * b + i] == 0xFFu) {
-#pragma unroll
-                  for (int t = 0; t < NT; ++t)
-                    if (t0 + 16 * e + 4 * kg + i < lim[t]) poison[t] |= 1u << b;
-                }
-            }
-            if (((g[e].vs >> (8 * i)) & 0xFFu) == 0xFFu) {
-#pragma unroll
-              for (int w = 0; w < VW / 4 + (VW < 4); ++w) {
-                if constexpr (VW >= 4) g[e].v[i * (VW / 4) + w] = 0;
-                else g[e].v[i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-              }
-              g[e].vs = (g[e].vs & ~(0xFFu << (8 * i))) | (0x7Fu << (8 * i));
-            }
-          }
+          for (int i = 0; i < 4; ++i)
+            if (nan_scale(vs[e], i)) drop(v[e], vs[e], i);
         }
       }
     }
 
-    // ---- scores, weights
-    bf16x8_t pf[NT][NP];
+    f32x4_t sa[NT][2];
     {
       bf16x8_t kf[2][KS];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float sc = __uint_as_float(g[e].ks << 23);
+        const float sc = __uint_as_float(ks[e] << 23);
 #pragma unroll
-        for (int s = 0; s < KS; ++s) kf[e][s] = eight<BK>(g[e].k + s * (BK / 4), sc);
+        for (int s = 0; s < KS; ++s) kf[e][s] = eight<BK>(k[e] + s * (BK / 4), sc);
       }
+      if (more) load_keys(step + 1, ((step + 1) ^ step) & 32);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        f32x4_t sa[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        sa[t][0] = sa[t][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = NP - 1; k >= 0; --k)  // small parts first
+        for (int kp = NP - 1; kp >= 0; --kp)  // small parts first
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            bf16x8_t q;
-            if constexpr (QL) q = __builtin_bit_cast(bf16x8_t, ql[((t * KS + s) * NP + k) * 64 + lane]);
-            else q = qf[t][s];
+          for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sa[e] = mfma(kf[e][s], q, sa[e]);
-          }
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int top = min(lim[t] - t0 - 16 * e, have[e]) - 4 * kg;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sa[e][i] = i < top ? sa[e][i] : -INFINITY;
-          }
-        }
-        float mx = fmaxf(fmaxf(fmaxf(sa[0][0], sa[0][1]), fmaxf(sa[0][2], sa[0][3])),
-                         fmaxf(fmaxf(sa[1][0], sa[1][1]), fmaxf(sa[1][2], sa[1][3])));
-        mx *= p.c;
-        if (__builtin_amdgcn_ballot_w64(mx > m[t] + kSlack)) {
-          mx = fmaxf(mx, __shfl_xor(mx, 16));
-          mx = fmaxf(mx, __shfl_xor(mx, 32));
-          const float nm = fmaxf(m[t], mx), a = __builtin_amdgcn_exp2f(m[t] - nm);
-          m[t] = nm;
-          l[t] *= a;
-#pragma unroll
-          for (int j = 0; j < C; ++j) acc[t][j] *= a;
-        }
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[i] = __builtin_amdgcn_exp2f(__fmaf_rn(sa[i / 4][i % 4], p.c, -m[t]));
-        }
-        l[t] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          uint32_t u[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            u[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
-            if (k + 1 < NP) {
-              w[2 * i] = rest(w[2 * i], u[i], 0);
-              w[2 * i + 1] = rest(w[2 * i + 1], u[i], 1);
-            }
-          }
-          pf[t][k] = operand(u[0], u[1], u[2], u[3]);
-        }
+            for (int e = 0; e < 2; ++e) sa[t][e] = mfma(kf[e][s], qf[t][s][kp], sa[t][e]);
       }
     }
-
-    // ---- values: channel pair (2 i, 2 i + 1) of the lane's entry at its
-    // four tokens of each page, then a word per channel and token pair
-    float vsc[2][4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vsc[e][i] = __uint_as_float(((g[e].vs >> (8 * i)) & 0xFFu) << 23);
-    auto value_pair = [&](int e, int i, auto ic) {
-      constexpr int c2 = decltype(ic)::value;  // channel pair
-      if constexpr (BV == 4 && C == 8) return two<4, c2>(g[e].v[i], vsc[e][i]);
-      else if constexpr (BV == 4) return (i & 1) ? two<4, 2 + c2>(g[e].v[i / 2], vsc[e][i]) : two<4, c2>(g[e].v[i / 2], vsc[e][i]);
-      else return two<8, c2 & 1>(g[e].v[i * (C / 4) + c2 / 2], vsc[e][i]);
-    };
-    auto channels = [&](auto ic) {
-      constexpr int c2 = decltype(ic)::value;
-      uint32_t x[2][4], ev[4], od[4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[e][i] = value_pair(e, i, ic);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          ev[2 * e + i] = __builtin_amdgcn_perm(x[e][2 * i + 1], x[e][2 * i], 0x05040100u);
-          od[2 * e + i] = __builtin_amdgcn_perm(x[e][2 * i + 1], x[e][2 * i], 0x07060302u);
-        }
-      const bf16x8_t ve = operand(ev[0], ev[1], ev[2], ev[3]), vo = operand(od[0], od[1], od[2], od[3]);
+    if (!whole) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = NP - 1; k >= 0; --k) {
-          acc[t][2 * c2] = mfma(ve, pf[t][k], acc[t][2 * c2]);
-          acc[t][2 * c2 + 1] = mfma(vo, pf[t][k], acc[t][2 * c2 + 1]);
+        for (int e = 0; e < 2; ++e) mask(sa[t][e], min(rw.lim[t] - t0 - 16 * e, have[e]) - 4 * kg);
+    }
+    bf16x8_t pf[NT][NP];
+    sm.step(sa, p.c, inv_c, acc, pf);
+
+    auto channels = [&](auto ic) {
+      constexpr int c2 = decltype(ic)::value;
+      uint32_t a[4], b[4];
+      value_words<D, BV, c2>(v[0], vs[0], a);
+      value_words<D, BV, c2>(v[1], vs[1], b);
+      const bf16x8_t ev = operand(a[0], a[1], b[0], b[1]), od = operand(a[2], a[3], b[2], b[3]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int kp = NP - 1; kp >= 0; --kp) {
+          acc[t][2 * c2] = mfma(ev, pf[t][kp], acc[t][2 * c2]);
+          acc[t][2 * c2 + 1] = mfma(od, pf[t][kp], acc[t][2 * c2 + 1]);
         }
     };
     channels(std::integral_constant<int, 0>{});
@@ -470,19 +542,20 @@ __global__ __launch_bounds__(256, 2) void k_mx_attn(const MxAttnParams p) {
       channels(std::integral_constant<int, 2>{});
       channels(std::integral_constant<int, 3>{});
     }
+    if (more) load_values();
   }
 
   // ---- join the waves, 16 rows at a time
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    float sum = l[t];
+    float sum = sm.l[t];
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
-    uint32_t pz = poison[t];
+    uint32_t pz = poison >> (4 * t);
     pz |= (uint32_t)__shfl_xor((int)pz, 16);
     pz |= (uint32_t)__shfl_xor((int)pz, 32);
     const bool dead = (pz >> (kg * (D / 32) / 4)) & 1u;  // this lane's channels [kg D / 4, (kg + 1) D / 4)
-    __syncthreads();                                     // the buffer is free
+    if (t) __syncthreads();                              // the buffer is free
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -491,12 +564,12 @@ __global__ __launch_bounds__(256, 2) void k_mx_attn(const MxAttnParams p) {
         if (dead) o = make_float4(NAN, NAN, NAN, NAN);
         *reinterpret_cast<float4*>(&lds[(wave * 16 + n) * OS + C * (4 * kg + i) + j]) = o;
       }
-    if (kg == 0) ml[wave][n] = make_float2(m[t], sum);
-    __syncthreads();
+    if (kg == 0) ml[wave][n] = make_float2(sm.m[t], sum);
     const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
-    const int2 rh = rowq[16 * t + r];
-    if (rh.x < 0) continue;
-    const int64_t at = (int64_t)rh.x * Hq + rh.y;
+    const int row = __shfl(rw.at[t], r), hq = __shfl(rw.head[t], r);
+    __syncthreads();
+    if (row < 0) continue;
+    const int64_t at = (int64_t)row * Hq + hq;
     float M = kLow, L = 0.f, a[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[w][r].x);
@@ -517,29 +590,222 @@ __global__ __launch_bounds__(256, 2) void k_mx_attn(const MxAttnParams p) {
         s.z = __fmaf_rn(a[w], x.z, s.z);
         s.w = __fmaf_rn(a[w], x.w, s.w);
       }
-      *reinterpret_cast<float4*>(o + j) = s;
+      o[j] = s.x;
+      o[j + 1] = s.y;
+      o[j + 2] = s.z;
+      o[j + 3] = s.w;
     }
-    if (p.ws_o) {
-      const int64_t slot = (int64_t)(p.slot0 + split) * p.b.total_rows * Hq + at;
-      float4* d = reinterpret_cast<float4*>(p.ws_o + slot * D + c0);
+    const int64_t slot = (int64_t)(p.slot0 + wk.split) * p.b.total_rows * Hq;
+    store_row<F32>(p.ws_o ? p.ws_o + slot * D : nullptr, p.out, at, D, c0, o, L);
+    if (c0 == 0) {
+      if (p.ws_o) p.ws_ml[slot + at] = make_float2(M, L);
+      else if (p.lse) p.lse[at] = log_sum(M, L);
+    }
+  }
+}
+
+// Many rows: bound by the matrix unit, the softmax and LDS.  A workgroup
+// takes 128 rows, 32 a wave, and walks over the tokens 64 at a time; each
+// wave turns one page of the next 64 tokens into operands in LDS, in the
+// order in which all four read them back, so a code is converted once for 128
+// rows.  Two buffers, one barrier per 64 tokens, no joining at the end.
+template <int D, int BK, int BV, bool F32>
+__global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
+  using Sh = Share<D, BK, BV>;
+  constexpr MxRecord R = Sh::R;
+  constexpr int C = D / 16, KS = D / 32, NP = F32 ? 3 : 1, NT = 2, TP = 4;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int n = lane & 15, kg = lane >> 4;
+  const Work wk = work_of(p);
+  const int h = wk.h;
+
+  __shared__ uint4 kbuf[2][TP][KS][64], vbuf[2][TP / 2][C][64];
+  __shared__ int4 info[2];  // per page: tokens that exist, bit 8 if a NaN value was taken out
+  __shared__ int2 bounds[4];
+
+  const int Hq = p.H * p.G;
+  MxSeq sq{0, 0, 0};
+  if (!p.prefix) sq = mx_seq(p.b, wk.z, p.status);
+  const int rows = (p.prefix ? p.b.total_rows : sq.n) * p.G;
+  if (wk.tile * 64 * NT >= rows) return;
+  const Rows<NT> rw = rows_of<NT>(p, sq, h, (wk.tile * 4 + wave) * 16 * NT, rows, n);
+  if (lane == 0) bounds[wave] = make_int2(rw.lo, rw.hi);
+  __syncthreads();
+  int lo = 0x7FFFFFFF, hi = 0;  // of all four waves
 #pragma unroll
-      for (int j = 0; j < C / 4; ++j) d[j] = *reinterpret_cast<const float4*>(o + 4 * j);
-      if (c0 == 0) p.ws_ml[slot] = make_float2(M, L);
-    } else {
-      const float r1 = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-      for (int j = 0; j < C; ++j) o[j] *= r1;
-      if constexpr (F32) {
-        float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at * D + c0);
-#pragma unroll
-        for (int j = 0; j < C / 4; ++j) d[j] = *reinterpret_cast<const float4*>(o + 4 * j);
-      } else {
-        uint2* d = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at * D + c0);
-#pragma unroll
-        for (int j = 0; j < C / 4; ++j)
-          d[j] = make_uint2(pack_bf16(o[4 * j], o[4 * j + 1]), pack_bf16(o[4 * j + 2], o[4 * j + 3]));
+  for (int w = 0; w < 4; ++w) {
+    lo = min(lo, bounds[w].x);
+    hi = max(hi, bounds[w].y);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  const int begin = p.begin + wk.split * p.chunk;
+  const int end = min(min(p.end, begin + p.chunk), hi);
+  if (p.ws_o && begin >= end) return;
+
+  const int32_t* table = p.b.page_table + (p.prefix ? 0 : (int64_t)wk.z * p.b.max_pages);
+  const uint8_t* head = p.pool + (int64_t)h * R.bytes;
+  const int64_t page_bytes = (int64_t)p.H * R.bytes;
+  const Sh sh(n, kg);
+  const int p0 = begin / KVTC_MX_PAGE, p1 = (end + KVTC_MX_PAGE - 1) / KVTC_MX_PAGE;
+  const int tiles = (p1 - p0 + TP - 1) / TP;
+
+  // this wave's pages p0 + 4 k + wave: the numbers of 64 tiles, one a lane
+  auto load_ids = [&](int k) {
+    const int pg = p0 + (k + lane) * TP + wave;
+    int id = -1;
+    if (pg < p1) {
+      id = table[pg];
+      if ((uint32_t)id >= (uint32_t)p.pool_pages) {
+        if (p.status) atomicOr(p.status, 1u << KVTC_ERR_INVALID_ARG);
+        id = -1;
       }
-      if (p.lse && c0 == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+    }
+    return id;
+  };
+  int ids = load_ids(0), ids2 = load_ids(64), id = -1;
+  uint32_t k[Sh::KW], v[Sh::VW], ks, vs;
+  auto load_page = [&](int t) {
+    if (t && (t & 63) == 0) {
+      ids = ids2;
+      ids2 = load_ids(t + 64);
+    }
+    id = __builtin_amdgcn_readlane(ids, t & 63);
+    const uint8_t* rec = head + max(id, 0) * page_bytes;
+    load_words(rec + sh.k, k);
+    load_words(rec + sh.v, v);
+    ks = rec[sh.ks];
+    vs = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
+  };
+  auto convert = [&](int t) {
+    const int b = t & 1, t0 = (p0 + t * TP + wave) * KVTC_MX_PAGE;
+    const int have = id < 0 ? 0 : min(max(end - t0, 0), 16);
+    int state = have;
+    if (have < 16 || t0 + 16 > lo) {  // as in k_mx_attn; the waves mark their own rows
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (4 * kg + i >= have) drop(v, vs, i);
+        if (nan_scale(vs, i)) {
+          nan = true;
+          drop(v, vs, i);
+        }
+      }
+      if (__builtin_amdgcn_ballot_w64(nan)) state |= 256;
+    }
+    if (lane == 0) reinterpret_cast<int*>(&info[b])[wave] = state;
+    const float sc = __uint_as_float(ks << 23);
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      kbuf[b][wave][s][lane] = __builtin_bit_cast(uint4, eight<BK>(k + s * (BK / 4), sc));
+    auto channels = [&](auto ic) {
+      constexpr int c2 = decltype(ic)::value;
+      uint32_t x[4];
+      value_words<D, BV, c2>(v, vs, x);
+      reinterpret_cast<uint2*>(&vbuf[b][wave / 2][2 * c2][lane])[wave & 1] = make_uint2(x[0], x[1]);
+      reinterpret_cast<uint2*>(&vbuf[b][wave / 2][2 * c2 + 1][lane])[wave & 1] = make_uint2(x[2], x[3]);
+    };
+    channels(std::integral_constant<int, 0>{});
+    channels(std::integral_constant<int, 1>{});
+    if constexpr (C == 8) {
+      channels(std::integral_constant<int, 2>{});
+      channels(std::integral_constant<int, 3>{});
+    }
+  };
+
+  bf16x8_t qf[NT][KS][NP];
+  load_queries<D, NT, F32>(p, rw, kg, qf);
+  f32x4_t acc[NT][C];
+  Softmax<NT, C, NP> sm;
+  const float inv_c = 1.0f / p.c;
+  uint32_t poison = 0;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  if (tiles > 0) {
+    load_page(0);
+    convert(0);
+    if (tiles > 1) load_page(1);
+  }
+  for (int t = 0; t < tiles; ++t) {
+    __syncthreads();  // tile t is in its buffer, nobody reads the other one
+    if (t + 1 < tiles) {
+      convert(t + 1);
+      if (t + 2 < tiles) load_page(t + 2);
+    }
+    const int b = t & 1;
+    const int4 in = info[b];
+    const int st[4] = {__builtin_amdgcn_readfirstlane(in.x), __builtin_amdgcn_readfirstlane(in.y),
+                       __builtin_amdgcn_readfirstlane(in.z), __builtin_amdgcn_readfirstlane(in.w)};
+#pragma unroll
+    for (int u = 0; u < TP / 2; ++u) {
+      const int t0 = (p0 + t * TP + 2 * u) * KVTC_MX_PAGE;
+      if (t0 >= rw.hi) break;  // this wave's rows end before
+      const int have[2] = {st[2 * u] & 255, st[2 * u + 1] & 255};
+      const bool whole = have[0] + have[1] == 32 && t0 + 32 <= rw.lo;
+      f32x4_t sa[NT][2];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) sa[i][0] = sa[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kp = NP - 1; kp >= 0; --kp)  // small parts first
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bf16x8_t kf = __builtin_bit_cast(bf16x8_t, kbuf[b][2 * u + e][s][lane]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sa[i][e] = mfma(kf, qf[i][s][kp], sa[i][e]);
+          }
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mask(sa[i][e], min(rw.lim[i] - t0 - 16 * e, have[e]) - 4 * kg);
+        if ((st[2 * u] | st[2 * u + 1]) & 256)
+          for (int e = 0; e < 2; ++e)
+            if (have[e] > 0)  // then its page is in the pool
+              mark_poison<D, NT>(head + table[t0 / KVTC_MX_PAGE + e] * page_bytes + R.kc + R.vc + R.sc + kg * (D / 32) * 4,
+                                 t0 + 16 * e + 4 * kg, have[e] - 4 * kg, rw.lim, poison);
+      }
+      bf16x8_t pf[NT][NP];
+      sm.step(sa, p.c, inv_c, acc, pf);
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vbuf[b][u][j][lane]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int kp = NP - 1; kp >= 0; --kp) acc[i][j] = mfma(vf, pf[i][kp], acc[i][j]);
+      }
+    }
+  }
+
+  // ---- a lane has channels [kg D / 4, (kg + 1) D / 4) of its row
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float sum = sm.l[t];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    uint32_t pz = poison >> (4 * t);
+    pz |= (uint32_t)__shfl_xor((int)pz, 16);
+    pz |= (uint32_t)__shfl_xor((int)pz, 32);
+    const bool dead = (pz >> (kg * (D / 32) / 4)) & 1u;
+    if (rw.at[t] < 0) continue;
+    const int64_t at = (int64_t)rw.at[t] * Hq + rw.head[t];
+    const int64_t slot = (int64_t)(p.slot0 + wk.split) * p.b.total_rows * Hq;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float o[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) o[j] = dead ? NAN : acc[t][j][i];
+      store_row<F32>(p.ws_o ? p.ws_o + slot * D : nullptr, p.out, at, D, C * (4 * kg + i), o, sum);
+    }
+    if (kg == 0) {
+      if (p.ws_o) p.ws_ml[slot + at] = make_float2(sm.m[t], sum);
+      else if (p.lse) p.lse[at] = log_sum(sm.m[t], sum);
     }
   }
 }
@@ -592,20 +858,8 @@ __global__ __launch_bounds__(256) void k_mx_join(const MxJoinParams p) {
     }
   }
   if (g) return;
-  const float r1 = L == 0.f ? 0.f : 1.0f / L;
-#pragma unroll
-  for (int j = 0; j < C; ++j) o[j] *= r1;
-  if constexpr (F32) {
-    float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at * D + c0);
-#pragma unroll
-    for (int j = 0; j < C / 4; ++j) d[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-  } else {
-    uint2* d = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at * D + c0);
-#pragma unroll
-    for (int j = 0; j < C / 4; ++j)
-      d[j] = make_uint2(pack_bf16(o[4 * j], o[4 * j + 1]), pack_bf16(o[4 * j + 2], o[4 * j + 3]));
-  }
-  if (p.lse && c0 == 0) p.lse[at] = L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * kLn2;
+  store_row<F32>(nullptr, p.out, at, D, c0, o, L);
+  if (p.lse && c0 == 0) p.lse[at] = log_sum(M, L);
 }
 
 template <int D, int BK, int BV>
@@ -613,11 +867,12 @@ hipError_t launch_attn(const MxAttnParams& p, bool f32, int nt, hipStream_t s) {
   const unsigned grid = (unsigned)p.H * p.tiles * p.nsplit * (p.prefix ? 1 : p.b.n_seqs);
   if (f32) {
     if (nt == 1) k_mx_attn<D, BK, BV, 1, true><<<grid, 256, 0, s>>>(p);
-    else k_mx_attn<D, BK, BV, 2, true><<<grid, 256, 0, s>>>(p);
+    else if (nt == 2) k_mx_attn<D, BK, BV, 2, true><<<grid, 256, 0, s>>>(p);
+    else k_mx_rows<D, BK, BV, true><<<grid, 256, 0, s>>>(p);
   } else {
     if (nt == 1) k_mx_attn<D, BK, BV, 1, false><<<grid, 256, 0, s>>>(p);
     else if (nt == 2) k_mx_attn<D, BK, BV, 2, false><<<grid, 256, 0, s>>>(p);
-    else k_mx_attn<D, BK, BV, 4, false><<<grid, 256, 0, s>>>(p);
+    else k_mx_rows<D, BK, BV, false><<<grid, 256, 0, s>>>(p);
   }
   return hipGetLastError();
 }

@@ -1,6 +1,7 @@
 // C ABI of the microscaled paged cache: argument checks, the split of the
 // attention over workgroups, and the launch sequences.
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 #include <utility>
@@ -122,11 +123,13 @@ struct Cut {
 };
 Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span, bool f32) {
   Cut c{};
-  c.nt = rows <= 16 ? 1 : rows <= 32 || f32 ? 2 : 4;
+  c.nt = rows <= 16 ? 1 : rows <= 64 ? 2 : 8;
+  (void)f32;
   c.tiles = (rows + 16 * c.nt - 1) / (16 * c.nt);
   // enough workgroups to fill the card four deep, none with fewer than 256 tokens
-  const int64_t units = c.tiles * H * seqs, want = (1024 + units - 1) / units;
-  const int64_t n = std::max<int64_t>(1, std::min(want, (span + 255) / 256));
+  static const int64_t target = getenv("MXT") ? atoi(getenv("MXT")) : 1024, hvy = getenv("MXH") ? atoi(getenv("MXH")) : 512, minc = getenv("MXC") ? atoi(getenv("MXC")) : 256;
+  const int64_t units = c.tiles * H * seqs, want = ((c.nt == 8 ? hvy : target) + units - 1) / units;
+  const int64_t n = std::max<int64_t>(1, std::min(want, (span + minc - 1) / minc));
   c.chunk = (int)(((span + n - 1) / n + 127) / 128 * 128);
   c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / std::max(c.chunk, 1));
   return c;
@@ -170,7 +173,7 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   st = plan_attn(*cfg, *b, q_heads, shared, &a);
   if (st != KVTC_OK) return st;
   const int elem = cfg->dtype == KVTC_BF16 ? 2 : 4;
-  if (!(scale > 0.0f) || !isfinite(scale) || (causal != 0 && causal != 1)) return KVTC_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !isnormal(scale) || (causal != 0 && causal != 1)) return KVTC_ERR_INVALID_ARG;
   if (q_stride < 0 || q_stride > ((int64_t)1 << 46) || (q_stride * elem) % 16) return KVTC_ERR_INVALID_ARG;
   if (nothing_to_do(*b)) return KVTC_OK;
   if (!q || !out || misaligned(q) || misaligned(out) || misaligned(lse, 4) || misaligned(ws)) return KVTC_ERR_INVALID_ARG;
