@@ -49,6 +49,9 @@ __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ float max2(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ float max3(float a, float b, float c) { return max2(max2(a, b), c); }
+
 // Two elements of a word as bf16 under a scale: pair i of its 8 / (B / 4).
 template <int B, int I>
 __device__ __forceinline__ uint32_t two(uint32_t w, float sc) {
@@ -70,7 +73,9 @@ __device__ __forceinline__ float rest(float x, uint32_t h, int hi) {
 
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[N]) {
-  if constexpr (N == 2) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(src);
+  } else if constexpr (N == 2) {
     const uint2 u = *reinterpret_cast<const uint2*>(src);
     w[0] = u.x;
     w[1] = u.y;
@@ -266,12 +271,17 @@ struct Softmax {
   }
   __device__ __forceinline__ void step(const f32x4_t (&s)[NT][2], float c, float inv_c, f32x4_t (&acc)[NT][C],
                                        bf16x8_t (&pf)[NT][NP]) {
+    vote(s, c, inv_c, acc);
+    weights(s, c, pf);
+  }
+  __device__ __forceinline__ void vote(const f32x4_t (&s)[NT][2], float c, float inv_c, f32x4_t (&acc)[NT][C]) {
     float mx[NT];
     bool up = false;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      mx[t] = fmaxf(fmaxf(fmaxf(s[t][0][0], s[t][0][1]), fmaxf(s[t][0][2], s[t][0][3])),
-                    fmaxf(fmaxf(s[t][1][0], s[t][1][1]), fmaxf(s[t][1][2], s[t][1][3])));
+      // NaN here leaves the maximum as it is: the row's sum becomes NaN anyway
+      mx[t] = max3(max3(s[t][0][0], s[t][0][1], s[t][0][2]), max3(s[t][0][3], s[t][1][0], s[t][1][1]),
+                   max2(s[t][1][2], s[t][1][3]));
       up |= mx[t] > raise[t];
     }
     if (__builtin_amdgcn_ballot_w64(up)) {
@@ -288,6 +298,8 @@ struct Softmax {
         for (int j = 0; j < C; ++j) acc[t][j] *= a;
       }
     }
+  }
+  __device__ __forceinline__ void weights(const f32x4_t (&s)[NT][2], float c, bf16x8_t (&pf)[NT][NP]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float w[8];
@@ -605,24 +617,30 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const 
 }
 
 // Many rows: bound by the matrix unit, the softmax and LDS.  A workgroup
-// takes 128 rows, 32 a wave, and walks over the tokens 64 at a time; each
-// wave turns one page of the next 64 tokens into operands in LDS, in the
-// order in which all four read them back, so a code is converted once for 128
-// rows.  Two buffers, one barrier per 64 tokens, no joining at the end.
+// takes 128 rows, 32 a wave, and walks over the tokens 32 at a time; each
+// wave turns half of a page into operands in LDS, in the order in which all
+// four read them back, so a code is converted once for 128 rows.  Three
+// buffers, so that in one stretch between barriers a wave multiplies the
+// keys of tile t + 1, weighs the scores of tile t, multiplies its values and
+// converts tile t + 2: matrix and vector work of the same wave overlap.
 template <int D, int BK, int BV, bool F32>
 __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
-  constexpr int C = D / 16, KS = D / 32, NP = F32 ? 3 : 1, NT = 2, TP = 4;
+  constexpr int C = D / 16, KS = D / 32, NP = F32 ? 3 : 1, NT = 2;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, kg = lane >> 4;
   const Work wk = work_of(p);
   const int h = wk.h;
 
-  __shared__ uint4 kbuf[2][TP][KS][64], vbuf[2][TP / 2][C][64];
-  __shared__ int4 info[2];  // per page: tokens that exist, bit 8 if a NaN value was taken out
+  struct Tile {
+    uint4 k[2][KS][64], v[C][64];
+    int2 state[2];  // per page and half: tokens that exist, bit 8 if a NaN value was taken out
+  };
+  __shared__ Tile tile[3];
   __shared__ int2 bounds[4];
+  __shared__ int odd;  // a page outside the pool was met: every tile's state is looked at
 
   const int Hq = p.H * p.G;
   MxSeq sq{0, 0, 0};
@@ -631,6 +649,7 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   if (wk.tile * 64 * NT >= rows) return;
   const Rows<NT> rw = rows_of<NT>(p, sq, h, (wk.tile * 4 + wave) * 16 * NT, rows, n);
   if (lane == 0) bounds[wave] = make_int2(rw.lo, rw.hi);
+  if (threadIdx.x == 0) odd = 0;
   __syncthreads();
   int lo = 0x7FFFFFFF, hi = 0;  // of all four waves
 #pragma unroll
@@ -649,74 +668,91 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   const int64_t page_bytes = (int64_t)p.H * R.bytes;
   const Sh sh(n, kg);
   const int p0 = begin / KVTC_MX_PAGE, p1 = (end + KVTC_MX_PAGE - 1) / KVTC_MX_PAGE;
-  const int tiles = (p1 - p0 + TP - 1) / TP;
+  const int tiles = (p1 - p0 + 1) / 2;
 
-  // this wave's pages p0 + 4 k + wave: the numbers of 64 tiles, one a lane
-  auto load_ids = [&](int k) {
-    const int pg = p0 + (k + lane) * TP + wave;
+  // This wave converts half `half` (of the contraction steps and of the
+  // channel pairs) of page p0 + 2 t + own of tile t: the numbers of 64 tiles,
+  // one a lane, the next 64 on their way; -1 as in k_mx_attn.
+  const int own = wave & 1, half = wave >> 1;
+  auto load_ids = [&](int t) {
+    const int pg = p0 + (t + lane) * 2 + own;
     int id = -1;
     if (pg < p1) {
       id = table[pg];
       if ((uint32_t)id >= (uint32_t)p.pool_pages) {
         if (p.status) atomicOr(p.status, 1u << KVTC_ERR_INVALID_ARG);
         id = -1;
+        odd = 1;
       }
     }
     return id;
   };
-  int ids = load_ids(0), ids2 = load_ids(64), id = -1;
-  uint32_t k[Sh::KW], v[Sh::VW], ks, vs;
-  auto load_page = [&](int t) {
+  int ids = load_ids(0), ids2 = load_ids(64);
+  auto id_of = [&](int t) {  // called for every t in turn
     if (t && (t & 63) == 0) {
       ids = ids2;
       ids2 = load_ids(t + 64);
     }
-    id = __builtin_amdgcn_readlane(ids, t & 63);
-    const uint8_t* rec = head + max(id, 0) * page_bytes;
-    load_words(rec + sh.k, k);
-    load_words(rec + sh.v, v);
-    ks = rec[sh.ks];
-    vs = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
+    return __builtin_amdgcn_readlane(ids, t & 63);
   };
-  auto convert = [&](int t) {
-    const int b = t & 1, t0 = (p0 + t * TP + wave) * KVTC_MX_PAGE;
-    const int have = id < 0 ? 0 : min(max(end - t0, 0), 16);
+  struct Raw {
+    int id;
+    uint32_t k[Sh::KW / 2], v[Sh::VW], ks, vs;
+  };
+  auto load_page = [&](Raw& g, int id) {
+    g.id = id;
+    const uint8_t* rec = head + max(id, 0) * page_bytes;
+    load_words(rec + sh.k + half * Sh::KW * 2, g.k);
+    load_words(rec + sh.v, g.v);
+    g.ks = rec[sh.ks];
+    g.vs = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
+  };
+  // what must not reach the products, as in k_mx_attn; each wave marks its own rows
+  auto clean = [&](Raw& g, int t, Tile& to) {
+    const int t0 = (p0 + 2 * t + own) * KVTC_MX_PAGE;
+    const int have = g.id < 0 ? 0 : min(max(end - t0, 0), 16);
     int state = have;
-    if (have < 16 || t0 + 16 > lo) {  // as in k_mx_attn; the waves mark their own rows
+    if (have < 16 || t0 + 16 > lo) {
       bool nan = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (4 * kg + i >= have) drop(v, vs, i);
-        if (nan_scale(vs, i)) {
+        if (4 * kg + i >= have) drop(g.v, g.vs, i);
+        if (nan_scale(g.vs, i)) {
           nan = true;
-          drop(v, vs, i);
+          drop(g.v, g.vs, i);
         }
       }
       if (__builtin_amdgcn_ballot_w64(nan)) state |= 256;
     }
-    if (lane == 0) reinterpret_cast<int*>(&info[b])[wave] = state;
-    const float sc = __uint_as_float(ks << 23);
+    if (lane == 0) reinterpret_cast<int*>(&to.state[own])[half] = state;
+  };
+  auto convert = [&](const Raw& g, Tile& to) {
+    const float sc = __uint_as_float(g.ks << 23);
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
-      kbuf[b][wave][s][lane] = __builtin_bit_cast(uint4, eight<BK>(k + s * (BK / 4), sc));
+    for (int s = 0; s < KS / 2; ++s)
+      to.k[own][half * (KS / 2) + s][lane] = __builtin_bit_cast(uint4, eight<BK>(g.k + s * (BK / 4), sc));
+    // the channel pairs of this half: the words move down, so that the pair is a constant
+    uint32_t y[Sh::VW];
+#pragma unroll
+    for (int i = 0; i < Sh::VW; ++i) {
+      if constexpr (BV == 8 && C == 8) y[i] = half ? g.v[i | 1] : g.v[i];
+      else y[i] = g.v[i] >> (half * (BV * C / 2));
+    }
     auto channels = [&](auto ic) {
       constexpr int c2 = decltype(ic)::value;
       uint32_t x[4];
-      value_words<D, BV, c2>(v, vs, x);
-      reinterpret_cast<uint2*>(&vbuf[b][wave / 2][2 * c2][lane])[wave & 1] = make_uint2(x[0], x[1]);
-      reinterpret_cast<uint2*>(&vbuf[b][wave / 2][2 * c2 + 1][lane])[wave & 1] = make_uint2(x[2], x[3]);
+      value_words<D, BV, c2>(y, g.vs, x);
+      const int c = half * (C / 2) + 2 * c2;
+      reinterpret_cast<uint2*>(&to.v[c][lane])[own] = make_uint2(x[0], x[1]);
+      reinterpret_cast<uint2*>(&to.v[c + 1][lane])[own] = make_uint2(x[2], x[3]);
     };
     channels(std::integral_constant<int, 0>{});
-    channels(std::integral_constant<int, 1>{});
-    if constexpr (C == 8) {
-      channels(std::integral_constant<int, 2>{});
-      channels(std::integral_constant<int, 3>{});
-    }
+    if constexpr (C == 8) channels(std::integral_constant<int, 1>{});
   };
 
   bf16x8_t qf[NT][KS][NP];
   load_queries<D, NT, F32>(p, rw, kg, qf);
-  f32x4_t acc[NT][C];
+  f32x4_t acc[NT][C], sa[NT][2];
   Softmax<NT, C, NP> sm;
   const float inv_c = 1.0f / p.c;
   uint32_t poison = 0;
@@ -724,63 +760,80 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int j = 0; j < C; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto scores = [&](const Tile& from, f32x4_t (&s)[NT][2]) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kp = NP - 1; kp >= 0; --kp)  // small parts first
+#pragma unroll
+      for (int c = 0; c < KS; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bf16x8_t kf = __builtin_bit_cast(bf16x8_t, from.k[e][c][lane]);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) s[i][e] = mfma(kf, qf[i][c][kp], s[i][e]);
+        }
+  };
 
+  Raw raw, ahead;  // codes of tile t + 2, and of t + 3 on their way
   if (tiles > 0) {
-    load_page(0);
-    convert(0);
-    if (tiles > 1) load_page(1);
+    load_page(raw, id_of(0));
+    load_page(ahead, id_of(1));
+    clean(raw, 0, tile[0]);
+    convert(raw, tile[0]);
+    load_page(raw, id_of(2));
+    clean(ahead, 1, tile[1]);
+    convert(ahead, tile[1]);
+    ahead = raw;
+    __syncthreads();
+    scores(tile[0], sa);
   }
+  int b = 0, slow = 0;  // buffer of tile t
   for (int t = 0; t < tiles; ++t) {
-    __syncthreads();  // tile t is in its buffer, nobody reads the other one
-    if (t + 1 < tiles) {
-      convert(t + 1);
-      if (t + 2 < tiles) load_page(t + 2);
+    Tile &now = tile[b], &next = tile[b == 2 ? 0 : b + 1], &after = tile[b == 0 ? 2 : b - 1];
+    const int t0 = (p0 + 2 * t) * KVTC_MX_PAGE;
+    // the page numbers of tile t were read at least 64 tiles, or the opening barrier, ago
+    if ((t & 63) == 0) slow = __builtin_amdgcn_readfirstlane(odd);
+    if (slow || t0 + 32 > min(end, rw.lo)) {
+      const int2 s0 = now.state[0], s1 = now.state[1];
+      const int st[2] = {__builtin_amdgcn_readfirstlane(s0.x | s0.y), __builtin_amdgcn_readfirstlane(s1.x | s1.y)};
+      const int have[2] = {st[0] & 255, st[1] & 255};
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mask(sa[i][e], min(rw.lim[i] - t0 - 16 * e, have[e]) - 4 * kg);
+      if ((st[0] | st[1]) & 256)
+        for (int e = 0; e < 2; ++e)
+          if (have[e] > 0)  // then its page is in the pool
+            mark_poison<D, NT>(head + table[t0 / KVTC_MX_PAGE + e] * page_bytes + R.kc + R.vc + R.sc + kg * (D / 32) * 4,
+                               t0 + 16 * e + 4 * kg, have[e] - 4 * kg, rw.lim, poison);
     }
-    const int b = t & 1;
-    const int4 in = info[b];
-    const int st[4] = {__builtin_amdgcn_readfirstlane(in.x), __builtin_amdgcn_readfirstlane(in.y),
-                       __builtin_amdgcn_readfirstlane(in.z), __builtin_amdgcn_readfirstlane(in.w)};
+    sm.vote(sa, p.c, inv_c, acc);
+    raw = ahead;
+    clean(raw, t + 2, after);
+    const int id = id_of(t + 3);
+    __syncthreads();  // tile t + 1 is in its buffer, nobody reads tile t - 1 any more
+    load_page(ahead, id);
+    __builtin_amdgcn_sched_barrier(0);  // the loads first
+    f32x4_t sb[NT][2];
+    scores(next, sb);
+    bf16x8_t pf[NT][NP];
+    sm.weights(sa, p.c, pf);
 #pragma unroll
-    for (int u = 0; u < TP / 2; ++u) {
-      const int t0 = (p0 + t * TP + 2 * u) * KVTC_MX_PAGE;
-      if (t0 >= rw.hi) break;  // this wave's rows end before
-      const int have[2] = {st[2 * u] & 255, st[2 * u + 1] & 255};
-      const bool whole = have[0] + have[1] == 32 && t0 + 32 <= rw.lo;
-      f32x4_t sa[NT][2];
+    for (int j = 0; j < C; ++j) {
+      const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, now.v[j][lane]);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) sa[i][0] = sa[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int kp = NP - 1; kp >= 0; --kp)  // small parts first
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bf16x8_t kf = __builtin_bit_cast(bf16x8_t, kbuf[b][2 * u + e][s][lane]);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) sa[i][e] = mfma(kf, qf[i][s][kp], sa[i][e]);
-          }
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) mask(sa[i][e], min(rw.lim[i] - t0 - 16 * e, have[e]) - 4 * kg);
-        if ((st[2 * u] | st[2 * u + 1]) & 256)
-          for (int e = 0; e < 2; ++e)
-            if (have[e] > 0)  // then its page is in the pool
-              mark_poison<D, NT>(head + table[t0 / KVTC_MX_PAGE + e] * page_bytes + R.kc + R.vc + R.sc + kg * (D / 32) * 4,
-                                 t0 + 16 * e + 4 * kg, have[e] - 4 * kg, rw.lim, poison);
-      }
-      bf16x8_t pf[NT][NP];
-      sm.step(sa, p.c, inv_c, acc, pf);
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vbuf[b][u][j][lane]);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int kp = NP - 1; kp >= 0; --kp) acc[i][j] = mfma(vf, pf[i][kp], acc[i][j]);
-      }
+        for (int kp = NP - 1; kp >= 0; --kp) acc[i][j] = mfma(vf, pf[i][kp], acc[i][j]);
     }
+    convert(raw, after);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      sa[i][0] = sb[i][0];
+      sa[i][1] = sb[i][1];
+    }
+    b = b == 2 ? 0 : b + 1;
   }
 
   // ---- a lane has channels [kg D / 4, (kg + 1) D / 4) of its row

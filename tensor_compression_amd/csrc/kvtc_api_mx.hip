@@ -1,7 +1,6 @@
 // C ABI of the microscaled paged cache: argument checks, the split of the
 // attention over workgroups, and the launch sequences.
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <utility>
@@ -117,19 +116,18 @@ kvtc_status io_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t l
 
 // How one pass of the attention is cut up.
 struct Cut {
-  int nt;           // 16-row tiles of a workgroup
-  int64_t tiles;    // workgroups along the rows
+  int nt;             // 16-row tiles of a workgroup: 1 or 2 (k_mx_attn), 8 (k_mx_rows)
+  int64_t tiles;      // workgroups along the rows
   int nsplit, chunk;  // workgroups along the tokens, tokens of each
 };
-Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span, bool f32) {
+Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span) {
   Cut c{};
   c.nt = rows <= 16 ? 1 : rows <= 64 ? 2 : 8;
-  (void)f32;
   c.tiles = (rows + 16 * c.nt - 1) / (16 * c.nt);
-  // enough workgroups to fill the card four deep, none with fewer than 256 tokens
-  static const int64_t target = getenv("MXT") ? atoi(getenv("MXT")) : 1024, hvy = getenv("MXH") ? atoi(getenv("MXH")) : 512, minc = getenv("MXC") ? atoi(getenv("MXC")) : 256;
-  const int64_t units = c.tiles * H * seqs, want = ((c.nt == 8 ? hvy : target) + units - 1) / units;
-  const int64_t n = std::max<int64_t>(1, std::min(want, (span + minc - 1) / minc));
+  // as many workgroups as the 256 CUs hold at once (4 each, 2 of those with
+  // more registers), none with fewer than 256 tokens
+  const int64_t units = c.tiles * H * seqs, room = c.nt == 1 ? 1024 : 512;
+  const int64_t n = std::max<int64_t>(1, std::min(room / units, (span + 255) / 256));
   c.chunk = (int)(((span + n - 1) / n + 127) / 128 * 128);
   c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / std::max(c.chunk, 1));
   return c;
@@ -148,11 +146,10 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   *a = AttnPlan{};
   if (nothing_to_do(b)) return KVTC_OK;
   const int G = q_heads / c.kv_heads;
-  const bool f32 = c.dtype == KVTC_FP32;
   a->begin = (int)std::min<int64_t>((int64_t)shared * KVTC_MX_PAGE, b.max_len);
   const int64_t rows = (int64_t)std::min(b.max_rows, b.total_rows) * G;
-  if (a->begin < b.max_len || a->begin == 0) a->own = cut_pass(rows, b.n_seqs, c.kv_heads, b.max_len - a->begin, f32);
-  if (a->begin > 0) a->prefix = cut_pass((int64_t)b.total_rows * G, 1, c.kv_heads, a->begin, f32);
+  if (a->begin < b.max_len || a->begin == 0) a->own = cut_pass(rows, b.n_seqs, c.kv_heads, b.max_len - a->begin);
+  if (a->begin > 0) a->prefix = cut_pass((int64_t)b.total_rows * G, 1, c.kv_heads, a->begin);
   a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
   if (a->own.tiles * c.kv_heads * std::max(a->own.nsplit, 1) * b.n_seqs > kMaxGrid ||

@@ -300,6 +300,29 @@ def test_attention_shared_prefix_many_rows():
         check_attention(c, q, out, lse, scale, causal, f"shared rows causal {causal}")
 
 
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_attention_long_ranges(dtype):
+    """Ranges of more pages than a workgroup knows the numbers of at once: few
+    rows (many sequences over the same pages leave no room to split) and many."""
+    n, H, ln = 64, 8, 17003
+    c = Case(128, 4, 4, dtype, H, [1], [ln], seed=21)
+    c.fill()
+    q = c.rand(n, H, 128)
+    table = c.table_dev.expand(n, -1).contiguous()
+    lens = [ln - 37 * z for z in range(n)]
+    b = c.cache.batch(table, dev(lens, torch.int32), dev(list(range(n + 1)), torch.int32), total_rows=n, max_rows=1, max_len=ln)
+    lse = torch.empty(n, H, device="cuda")
+    out, _ = c.cache.attention(b, q, lse=lse, status=c.status)
+    for z in (0, 41, 63):
+        c.lens = [lens[z]]
+        check_attention(c, q[z:z + 1], out[z:z + 1], lse[z:z + 1], 128 ** -0.5, True, f"long range {z} dtype {dtype}")
+    c = Case(64, 8, 4, dtype, 8, [300], [5003], seed=22)
+    c.fill()
+    q, out, lse, scale = run_attention(c, 1)
+    check_attention(c, q, out, lse, scale, True, f"long rows dtype {dtype}")
+    assert c.status.item() == 0
+
+
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 8.0])
 def test_attention_scales(scale):
     """Flat and needle-sharp weights, scores that grow along the sequence."""
