@@ -71,22 +71,31 @@ __device__ __forceinline__ float rest(float x, uint32_t h, int hi) {
   return x - __uint_as_float(hi ? h & 0xFFFF0000u : h << 16);
 }
 
-template <int N>
+// Codes on their way in; ONCE: past the caches, where no other workgroup reads
+// them and they are more than the memory-side cache could keep for the next
+// call (64 ragged sequences, 309 MB: 72 -> 67 us; 16 of 8000 tokens, 139 MB
+// and so still there when read again: 28 -> 36 us, so those are cached).
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+template <bool ONCE, typename T>
+__device__ __forceinline__ T load(const uint8_t* src) {
+  const T* s = reinterpret_cast<const T*>(src);
+  if constexpr (ONCE) return __builtin_nontemporal_load(s);
+  else return *s;
+}
+template <bool ONCE, int N>
 __device__ __forceinline__ void load_words(const uint8_t* src, uint32_t (&w)[N]) {
-  if constexpr (N == 1) {
-    w[0] = *reinterpret_cast<const uint32_t*>(src);
-  } else if constexpr (N == 2) {
-    const uint2 u = *reinterpret_cast<const uint2*>(src);
-    w[0] = u.x;
-    w[1] = u.y;
+  if constexpr (N == 1) w[0] = load<ONCE, uint32_t>(src);
+  else if constexpr (N == 2) {
+    const u32x2_t u = load<ONCE, u32x2_t>(src);
+    w[0] = u[0];
+    w[1] = u[1];
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const uint4 u = reinterpret_cast<const uint4*>(src)[i];
-      w[4 * i] = u.x;
-      w[4 * i + 1] = u.y;
-      w[4 * i + 2] = u.z;
-      w[4 * i + 3] = u.w;
+      const u32x4_t u = load<ONCE, u32x4_t>(src + 16 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = u[j];
     }
   }
 }
@@ -376,8 +385,8 @@ __device__ __forceinline__ Work work_of(const MxAttnParams& p) {
 // Few rows: memory bound, one pass over the codes with as many loads in
 // flight as the registers allow.  The waves take pairs of pages in turn, all
 // for the same 16 NT rows, and are joined at the end.
-template <int D, int BK, int BV, int NT, bool F32>
-__global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const MxAttnParams p) {
+template <int D, int BK, int BV, int NT, bool F32, bool ONCE>
+__global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const MxAttnParams p) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
   constexpr int C = D / 16;       // channels of an entry of the value groups
@@ -429,7 +438,8 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const 
   };
   // A lane's share of a step's two pages as it lies in their records.  The
   // keys of the next step are requested as soon as this step's have become
-  // operands, its values at the end of this step.
+  // operands, its values at the end of this step (after the last step, page 0:
+  // a condition would make the loop wait for the loads).
   int id[2];
   uint32_t k[2][Sh::KW], v[2][Sh::VW], ks[2], vs[2];
   int ids = load_ids(0), ids2 = load_ids(32);
@@ -438,16 +448,16 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const 
     for (int e = 0; e < 2; ++e) {
       id[e] = __builtin_amdgcn_readlane(later ? ids2 : ids, 2 * (step & 31) + e);
       const uint8_t* rec = head + max(id[e], 0) * page_bytes;
-      load_words(rec + sh.k, k[e]);
-      ks[e] = rec[sh.ks];
+      load_words<ONCE>(rec + sh.k, k[e]);
+      ks[e] = load<ONCE, uint8_t>(rec + sh.ks);
     }
   };
   auto load_values = [&]() {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const uint8_t* rec = head + max(id[e], 0) * page_bytes;
-      load_words(rec + sh.v, v[e]);
-      vs[e] = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
+      load_words<ONCE>(rec + sh.v, v[e]);
+      vs[e] = load<ONCE, uint32_t>(rec + sh.vs);
     }
   };
 
@@ -473,7 +483,6 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const 
       ids2 = load_ids(step + 32);
     }
     const int t0 = (q0 + 8 * step) * KVTC_MX_PAGE;
-    const bool more = step + 1 < steps;
     // tokens of page e that exist for this workgroup, 0 .. 16
     int have[2];
 #pragma unroll
@@ -513,7 +522,7 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const 
 #pragma unroll
         for (int s = 0; s < KS; ++s) kf[e][s] = eight<BK>(k[e] + s * (BK / 4), sc);
       }
-      if (more) load_keys(step + 1, ((step + 1) ^ step) & 32);
+      load_keys(step + 1, ((step + 1) ^ step) & 32);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         sa[t][0] = sa[t][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -554,7 +563,7 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 4 : 2) void k_mx_attn(const 
       channels(std::integral_constant<int, 2>{});
       channels(std::integral_constant<int, 3>{});
     }
-    if (more) load_values();
+    load_values();
   }
 
   // ---- join the waves, 16 rows at a time
@@ -702,8 +711,8 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   auto load_page = [&](Raw& g, int id) {
     g.id = id;
     const uint8_t* rec = head + max(id, 0) * page_bytes;
-    load_words(rec + sh.k + half * Sh::KW * 2, g.k);
-    load_words(rec + sh.v, g.v);
+    load_words<false>(rec + sh.k + half * Sh::KW * 2, g.k);
+    load_words<false>(rec + sh.v, g.v);
     g.ks = rec[sh.ks];
     g.vs = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
   };
@@ -863,13 +872,14 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   }
 }
 
-// Joins a row's partials: one wave a (row, head), sixteen lanes on its
-// channels, four partials at once.
-template <int D, bool F32>
+// Joins a row's partials: W waves a (row, head), sixteen lanes on its
+// channels, so 4 W partials at once; W = 4 where there are many.
+template <int D, bool F32, int W>
 __global__ __launch_bounds__(256) void k_mx_join(const MxJoinParams p) {
   constexpr int C = D / 16;
-  const int lane = threadIdx.x & 63, g = lane >> 4, c0 = (lane & 15) * C;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c0 = (lane & 15) * C;
+  const int g = (W == 4 ? wave * 4 : 0) + (lane >> 4);
+  const int64_t at = W == 4 ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
   const int64_t all = (int64_t)p.b.total_rows * p.Hq;
   if (at >= all) return;
   const int row = (int)(at / p.Hq);
@@ -882,75 +892,99 @@ __global__ __launch_bounds__(256) void k_mx_join(const MxJoinParams p) {
   float M = kLow, L = 0.f, o[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) o[j] = 0.f;
-  for (int k = g; k < a + b; k += 4) {
+  auto add = [&](float m, float l, const float (&v)[C]) {
+    const float nm = fmaxf(M, m), u = __builtin_amdgcn_exp2f(M - nm), w = __builtin_amdgcn_exp2f(m - nm);
+    M = nm;
+    L = __fmaf_rn(L, u, l * w);
+#pragma unroll
+    for (int j = 0; j < C; ++j) o[j] = __fmaf_rn(o[j], u, v[j] * w);
+  };
+#pragma unroll 2
+  for (int k = g; k < a + b; k += 4 * W) {
     const int64_t slot = (int64_t)(k < a ? k : p.prefix_splits + k - a) * all + at;
     const float2 x = p.ws_ml[slot];
-    const float nm = fmaxf(M, x.x), u = __builtin_amdgcn_exp2f(M - nm), w = __builtin_amdgcn_exp2f(x.x - nm);
-    M = nm;
-    L = __fmaf_rn(L, u, x.y * w);
     const float4* y = reinterpret_cast<const float4*>(p.ws_o + slot * D + c0);
+    float v[C];
 #pragma unroll
     for (int j = 0; j < C / 4; ++j) {
-      const float4 v = y[j];
-      o[4 * j] = __fmaf_rn(o[4 * j], u, v.x * w);
-      o[4 * j + 1] = __fmaf_rn(o[4 * j + 1], u, v.y * w);
-      o[4 * j + 2] = __fmaf_rn(o[4 * j + 2], u, v.z * w);
-      o[4 * j + 3] = __fmaf_rn(o[4 * j + 3], u, v.w * w);
+      const float4 t = y[j];
+      v[4 * j] = t.x;
+      v[4 * j + 1] = t.y;
+      v[4 * j + 2] = t.z;
+      v[4 * j + 3] = t.w;
     }
+    add(x.x, x.y, v);
   }
 #pragma unroll
   for (int d = 16; d < 64; d <<= 1) {
-    const float om = __shfl_xor(M, d), nm = fmaxf(M, om), u = __builtin_amdgcn_exp2f(M - nm);
-    M = nm;
-    L *= u;
-    L += __shfl_xor(L, d);
+    const float m = __shfl_xor(M, d), l = __shfl_xor(L, d);
+    float v[C];
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      o[j] *= u;
-      o[j] += __shfl_xor(o[j], d);
+    for (int j = 0; j < C; ++j) v[j] = __shfl_xor(o[j], d);
+    add(m, l, v);
+  }
+  if constexpr (W == 4) {
+    __shared__ float part[3][16][C + 2];
+    if (wave > 0 && lane < 16) {
+      part[wave - 1][lane][0] = M;
+      part[wave - 1][lane][1] = L;
+#pragma unroll
+      for (int j = 0; j < C; ++j) part[wave - 1][lane][2 + j] = o[j];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < 3; ++w) {
+      float v[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = part[w][lane & 15][2 + j];
+      add(part[w][lane & 15][0], part[w][lane & 15][1], v);
     }
   }
-  if (g) return;
+  if (lane >= 16) return;
   store_row<F32>(nullptr, p.out, at, D, c0, o, L);
   if (p.lse && c0 == 0) p.lse[at] = log_sum(M, L);
 }
 
+template <int D, int BK, int BV, bool F32>
+void launch_format(const MxAttnParams& p, unsigned grid, hipStream_t s) {
+  if (p.nt == 1) {
+    if (p.once) k_mx_attn<D, BK, BV, 1, F32, true><<<grid, 256, 0, s>>>(p);
+    else k_mx_attn<D, BK, BV, 1, F32, false><<<grid, 256, 0, s>>>(p);
+  } else if (p.nt == 2) k_mx_attn<D, BK, BV, 2, F32, false><<<grid, 256, 0, s>>>(p);
+  else k_mx_rows<D, BK, BV, F32><<<grid, 256, 0, s>>>(p);
+}
 template <int D, int BK, int BV>
-hipError_t launch_attn(const MxAttnParams& p, bool f32, int nt, hipStream_t s) {
+hipError_t launch_attn(const MxAttnParams& p, bool f32, hipStream_t s) {
   const unsigned grid = (unsigned)p.H * p.tiles * p.nsplit * (p.prefix ? 1 : p.b.n_seqs);
-  if (f32) {
-    if (nt == 1) k_mx_attn<D, BK, BV, 1, true><<<grid, 256, 0, s>>>(p);
-    else if (nt == 2) k_mx_attn<D, BK, BV, 2, true><<<grid, 256, 0, s>>>(p);
-    else k_mx_rows<D, BK, BV, true><<<grid, 256, 0, s>>>(p);
-  } else {
-    if (nt == 1) k_mx_attn<D, BK, BV, 1, false><<<grid, 256, 0, s>>>(p);
-    else if (nt == 2) k_mx_attn<D, BK, BV, 2, false><<<grid, 256, 0, s>>>(p);
-    else k_mx_rows<D, BK, BV, false><<<grid, 256, 0, s>>>(p);
-  }
+  f32 ? launch_format<D, BK, BV, true>(p, grid, s) : launch_format<D, BK, BV, false>(p, grid, s);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_mx_attn(const MxAttnParams& p, int D, int bk, int bv, bool f32, int nt, hipStream_t s) {
+hipError_t launch_mx_attn(const MxAttnParams& p, int D, int bk, int bv, bool f32, hipStream_t s) {
   if (D == 128) {
-    if (bk == 4) return bv == 4 ? launch_attn<128, 4, 4>(p, f32, nt, s) : launch_attn<128, 4, 8>(p, f32, nt, s);
-    return bv == 4 ? launch_attn<128, 8, 4>(p, f32, nt, s) : launch_attn<128, 8, 8>(p, f32, nt, s);
+    if (bk == 4) return bv == 4 ? launch_attn<128, 4, 4>(p, f32, s) : launch_attn<128, 4, 8>(p, f32, s);
+    return bv == 4 ? launch_attn<128, 8, 4>(p, f32, s) : launch_attn<128, 8, 8>(p, f32, s);
   }
-  if (bk == 4) return bv == 4 ? launch_attn<64, 4, 4>(p, f32, nt, s) : launch_attn<64, 4, 8>(p, f32, nt, s);
-  return bv == 4 ? launch_attn<64, 8, 4>(p, f32, nt, s) : launch_attn<64, 8, 8>(p, f32, nt, s);
+  if (bk == 4) return bv == 4 ? launch_attn<64, 4, 4>(p, f32, s) : launch_attn<64, 4, 8>(p, f32, s);
+  return bv == 4 ? launch_attn<64, 8, 4>(p, f32, s) : launch_attn<64, 8, 8>(p, f32, s);
+}
+
+template <int D, bool F32>
+static void launch_join(const MxJoinParams& p, hipStream_t s) {
+  const int64_t all = (int64_t)p.b.total_rows * p.Hq;
+  // one wave a row is done in two rounds of loads up to 8 partials; more of
+  // them are worth the barrier while there are few rows (64 rows of 32
+  // partials: 6.2 -> 4.6 us, but 2048 rows of 33: 8.2 -> 9.4 us)
+  if (p.prefix_splits + p.nsplit > 8 && all <= 512) k_mx_join<D, F32, 4><<<(unsigned)all, 256, 0, s>>>(p);
+  else k_mx_join<D, F32, 1><<<(unsigned)((all + 3) / 4), 256, 0, s>>>(p);
 }
 
 hipError_t launch_mx_join(const MxJoinParams& p, bool f32, hipStream_t s) {
-  const int64_t all = (int64_t)p.b.total_rows * p.Hq;
-  const unsigned grid = (unsigned)((all + 3) / 4);
-  if (p.D == 128) {
-    if (f32) k_mx_join<128, true><<<grid, 256, 0, s>>>(p);
-    else k_mx_join<128, false><<<grid, 256, 0, s>>>(p);
-  } else {
-    if (f32) k_mx_join<64, true><<<grid, 256, 0, s>>>(p);
-    else k_mx_join<64, false><<<grid, 256, 0, s>>>(p);
-  }
+  if (p.D == 128) f32 ? launch_join<128, true>(p, s) : launch_join<128, false>(p, s);
+  else f32 ? launch_join<64, true>(p, s) : launch_join<64, false>(p, s);
   return hipGetLastError();
 }
 

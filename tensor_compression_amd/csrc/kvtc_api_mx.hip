@@ -124,10 +124,13 @@ Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span) {
   Cut c{};
   c.nt = rows <= 16 ? 1 : rows <= 64 ? 2 : 8;
   c.tiles = (rows + 16 * c.nt - 1) / (16 * c.nt);
-  // as many workgroups as the 256 CUs hold at once (4 each, 2 of those with
-  // more registers), none with fewer than 256 tokens
-  const int64_t units = c.tiles * H * seqs, room = c.nt == 1 ? 1024 : 512;
-  const int64_t n = std::max<int64_t>(1, std::min(room / units, (span + 255) / 256));
+  // As many workgroups as the card takes at its rate: one a CU for few rows
+  // (1 sequence of 131072 tokens: 41 us with 256, 42 with 768, and more
+  // partials to join), two for many rows, which need the second's waves.
+  // Short sequences stay whole: a step of 128 tokens costs 0.55 us, a second
+  // launch and its join 2.8 us.
+  const int64_t units = c.tiles * H * seqs, room = c.nt == 8 ? 512 : 256;
+  const int64_t n = span <= 640 ? 1 : std::max<int64_t>(1, std::min(room / units, (span + 127) / 128));
   c.chunk = (int)(((span + n - 1) / n + 127) / 128 * 128);
   c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / std::max(c.chunk, 1));
   return c;
@@ -154,7 +157,7 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
   if (a->own.tiles * c.kv_heads * std::max(a->own.nsplit, 1) * b.n_seqs > kMaxGrid ||
       a->prefix.tiles * c.kv_heads * std::max(a->prefix.nsplit, 1) > kMaxGrid ||
-      ((int64_t)b.total_rows * q_heads + 3) / 4 > kMaxGrid)
+      (int64_t)b.total_rows * q_heads > 4 * kMaxGrid)
     return KVTC_ERR_UNSUPPORTED;
   return KVTC_OK;
 }
@@ -198,7 +201,8 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
     p.tiles = (int32_t)c.tiles;
     p.nsplit = c.nsplit;
     p.chunk = c.chunk;
-    return launch_mx_attn(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, f32, c.nt, stream);
+    p.nt = c.nt;
+    return launch_mx_attn(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, f32, stream);
   };
   if (a.prefix.nsplit) {
     p.prefix = 1;
@@ -206,6 +210,9 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
     if (pass(a.prefix) != hipSuccess) return KVTC_ERR_HIP;
     p.prefix = 0;
   }
+  // at most this many bytes of codes, against the 256 MB of the memory-side cache
+  p.once = (int64_t)b->n_seqs * (b->max_len - a.begin) / KVTC_MX_PAGE * cfg->kv_heads *
+               mx_record(cfg->head_dim, cfg->bits_k, cfg->bits_v).bytes > ((int64_t)256 << 20);
   p.begin = a.begin;
   p.end = 0x7FFFFFFF;
   p.slot0 = a.prefix.nsplit;
