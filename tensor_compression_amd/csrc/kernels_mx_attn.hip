@@ -30,6 +30,7 @@ namespace kvtc {
 
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
@@ -47,6 +48,9 @@ __device__ __forceinline__ bf16x8_t operand(uint32_t a, uint32_t b, uint32_t c, 
 }
 __device__ __forceinline__ f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mfma(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
 __device__ __forceinline__ float max2(float a, float b) { return __builtin_elementwise_maximum(a, b); }
@@ -169,41 +173,40 @@ __device__ __forceinline__ Rows<NT> rows_of(const MxAttnParams& p, const MxSeq& 
   return o;
 }
 
-// Query operands: channels (D / 4) kg + 8 s .. + 7 of the lane's row, as bf16
-// or as three bf16 parts.
-template <int D, int NT, bool F32>
-__device__ __forceinline__ void load_queries(const MxAttnParams& p, const Rows<NT>& rw, int kg,
-                                             bf16x8_t (&q)[NT][D / 32][F32 ? 3 : 1]) {
+// Eight fp32 values as one bf16 operand, or as three whose sum keeps 24 bits.
+template <int NP>
+__device__ __forceinline__ void split8(float (&x)[8], bf16x8_t (&o)[NP]) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t off = rw.at[t] * p.q_stride + rw.head[t] * D + (D / 4) * kg;
+  for (int k = 0; k < NP; ++k) {
+    uint32_t u[4];
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-      if constexpr (!F32) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (rw.at[t] >= 0) w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + off + 8 * s);
-        q[t][s][0] = __builtin_bit_cast(bf16x8_t, w);
-      } else {
-        float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        if (rw.at[t] >= 0) {
-          const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + off + 8 * s);
-          x[0] = src[0];
-          x[1] = src[1];
-        }
-        float f[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          uint32_t u[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            u[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-            f[2 * i] = rest(f[2 * i], u[i], 0);
-            f[2 * i + 1] = rest(f[2 * i + 1], u[i], 1);
-          }
-          q[t][s][k] = operand(u[0], u[1], u[2], u[3]);
-        }
+    for (int i = 0; i < 4; ++i) {
+      u[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+      if (k + 1 < NP) {
+        x[2 * i] = rest(x[2 * i], u[i], 0);
+        x[2 * i + 1] = rest(x[2 * i + 1], u[i], 1);
       }
     }
+    o[k] = operand(u[0], u[1], u[2], u[3]);
+  }
+}
+
+// A query operand: 8 channels at `off` of q, zeros for no row.
+template <bool F32>
+__device__ __forceinline__ void load_query(const MxAttnParams& p, int64_t off, bool on, bf16x8_t (&q)[F32 ? 3 : 1]) {
+  if constexpr (!F32) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (on) w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + off);
+    q[0] = __builtin_bit_cast(bf16x8_t, w);
+  } else {
+    float4 x[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (on) {
+      const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + off);
+      x[0] = src[0];
+      x[1] = src[1];
+    }
+    float f[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    split8<3>(f, q);
   }
 }
 
@@ -280,10 +283,6 @@ struct Softmax {
   }
   __device__ __forceinline__ void step(const f32x4_t (&s)[NT][2], float c, float inv_c, f32x4_t (&acc)[NT][C],
                                        bf16x8_t (&pf)[NT][NP]) {
-    vote(s, c, inv_c, acc);
-    weights(s, c, pf);
-  }
-  __device__ __forceinline__ void vote(const f32x4_t (&s)[NT][2], float c, float inv_c, f32x4_t (&acc)[NT][C]) {
     float mx[NT];
     bool up = false;
 #pragma unroll
@@ -307,27 +306,13 @@ struct Softmax {
         for (int j = 0; j < C; ++j) acc[t][j] *= a;
       }
     }
-  }
-  __device__ __forceinline__ void weights(const f32x4_t (&s)[NT][2], float c, bf16x8_t (&pf)[NT][NP]) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = __builtin_amdgcn_exp2f(__fmaf_rn(s[t][i / 4][i % 4], c, -m[t]));
       l[t] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-#pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        uint32_t x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = pack_bf16(w[2 * i], w[2 * i + 1]);
-          if (k + 1 < NP) {
-            w[2 * i] = rest(w[2 * i], x[i], 0);
-            w[2 * i + 1] = rest(w[2 * i + 1], x[i], 1);
-          }
-        }
-        pf[t][k] = operand(x[0], x[1], x[2], x[3]);
-      }
+      split8<NP>(w, pf[t]);
     }
   }
 };
@@ -462,7 +447,12 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
   };
 
   bf16x8_t qf[NT][KS][NP];
-  load_queries<D, NT, F32>(p, rw, kg, qf);
+  // channels (D / 4) kg + 8 s .. + 7 of the lane's rows
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+      load_query<F32>(p, rw.at[t] * p.q_stride + rw.head[t] * D + (D / 4) * kg + 8 * s, rw.at[t] >= 0, qf[t][s]);
   if (steps > 0) {
     load_keys(0, false);
     load_values();
@@ -625,27 +615,35 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
   }
 }
 
-// Many rows: bound by the matrix unit, the softmax and LDS.  A workgroup
-// takes 128 rows, 32 a wave, and walks over the tokens 32 at a time; each
-// wave turns half of a page into operands in LDS, in the order in which all
-// four read them back, so a code is converted once for 128 rows.  Three
-// buffers, so that in one stretch between barriers a wave multiplies the
-// keys of tile t + 1, weighs the scores of tile t, multiplies its values and
-// converts tile t + 2: matrix and vector work of the same wave overlap.
+// Many rows: bound by the issue of matrix and vector instructions.  A
+// workgroup takes 128 rows, 32 a wave, and walks over the tokens 32 at a
+// time; each wave turns half of a page into operands in LDS, in the order in
+// which all four read them back, so a code is converted once for 128 rows.
+// Three buffers, so that in one stretch between barriers a wave multiplies
+// the keys of tile t + 1, weighs the scores of tile t, multiplies its values
+// and converts tile t + 2: matrix and vector work of the same wave overlap.
+//
+// v_mfma_f32_32x32x16_bf16 (half the instructions of the 16-row form): S^T
+// has the two pages' tokens as rows; lane (hh, q) = (lane / 32, lane % 32)
+// gets tokens 4 hh .. + 3 and 8 + 4 hh .. + 3 of each page for query row q,
+// the slice of P^T that the product with 16 tokens' values takes from it.
+// Value rows of a 32-channel product: row n + 16 o is channel 2 ct + o of
+// entry n of the value groups.
 template <int D, int BK, int BV, bool F32>
 __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
-  constexpr int C = D / 16, KS = D / 32, NP = F32 ? 3 : 1, NT = 2;
+  constexpr int C = D / 16, KS = D / 32, QS = D / 16, CT = D / 32, NP = F32 ? 3 : 1;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int n = lane & 15, kg = lane >> 4;
+  const int n = lane & 15, kg = lane >> 4, hh = lane >> 5;
   const Work wk = work_of(p);
   const int h = wk.h;
 
   struct Tile {
-    uint4 k[2][KS][64], v[C][64];
-    int2 state[2];  // per page and half: tokens that exist, bit 8 if a NaN value was taken out
+    uint4 k[QS][64];      // contraction step, operand lane
+    uint4 v[2][CT][64];   // page, channel tile, operand lane
+    int2 state[2];        // per page and half: tokens that exist, bit 8 if a NaN value was taken out
   };
   __shared__ Tile tile[3];
   __shared__ int2 bounds[4];
@@ -655,8 +653,13 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   MxSeq sq{0, 0, 0};
   if (!p.prefix) sq = mx_seq(p.b, wk.z, p.status);
   const int rows = (p.prefix ? p.b.total_rows : sq.n) * p.G;
-  if (wk.tile * 64 * NT >= rows) return;
-  const Rows<NT> rw = rows_of<NT>(p, sq, h, (wk.tile * 4 + wave) * 16 * NT, rows, n);
+  if (wk.tile * 128 >= rows) return;
+  Rows<1> rw = rows_of<1>(p, sq, h, wk.tile * 128 + wave * 32, rows, lane & 31);
+  {  // rows_of looks at the first 16 lanes
+    const int lo = rw.at[0] >= 0 ? rw.lim[0] : 0x7FFFFFFF;
+    rw.lo = min(rw.lo, __builtin_amdgcn_readlane(row_min(lo), 16));
+    rw.hi = max(rw.hi, __builtin_amdgcn_readlane(row_max(rw.lim[0]), 16));
+  }
   if (lane == 0) bounds[wave] = make_int2(rw.lo, rw.hi);
   if (threadIdx.x == 0) odd = 0;
   __syncthreads();
@@ -679,7 +682,7 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   const int p0 = begin / KVTC_MX_PAGE, p1 = (end + KVTC_MX_PAGE - 1) / KVTC_MX_PAGE;
   const int tiles = (p1 - p0 + 1) / 2;
 
-  // This wave converts half `half` (of the contraction steps and of the
+  // This wave converts half `half` (of a lane's key channels and of the value
   // channel pairs) of page p0 + 2 t + own of tile t: the numbers of 64 tiles,
   // one a lane, the next 64 on their way; -1 as in k_mx_attn.
   const int own = wave & 1, half = wave >> 1;
@@ -738,8 +741,10 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
   auto convert = [&](const Raw& g, Tile& to) {
     const float sc = __uint_as_float(g.ks << 23);
 #pragma unroll
-    for (int s = 0; s < KS / 2; ++s)
-      to.k[own][half * (KS / 2) + s][lane] = __builtin_bit_cast(uint4, eight<BK>(g.k + s * (BK / 4), sc));
+    for (int i = 0; i < KS / 2; ++i) {  // channels 8 f .. + 7 of the lane's quarter: step f / 2, lane half f % 2
+      const int f = half * (KS / 2) + i;
+      to.k[(kg * KS + f) >> 1][(f & 1) * 32 + own * 16 + n] = __builtin_bit_cast(uint4, eight<BK>(g.k + i * (BK / 4), sc));
+    }
     // the channel pairs of this half: the words move down, so that the pair is a constant
     uint32_t y[Sh::VW];
 #pragma unroll
@@ -751,37 +756,34 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
       constexpr int c2 = decltype(ic)::value;
       uint32_t x[4];
       value_words<D, BV, c2>(y, g.vs, x);
-      const int c = half * (C / 2) + 2 * c2;
-      reinterpret_cast<uint2*>(&to.v[c][lane])[own] = make_uint2(x[0], x[1]);
-      reinterpret_cast<uint2*>(&to.v[c + 1][lane])[own] = make_uint2(x[2], x[3]);
+      uint4* const to_v = &to.v[own][half * (C / 4) + c2][(kg & 1) * 32 + n];
+      reinterpret_cast<uint2*>(to_v)[kg >> 1] = make_uint2(x[0], x[1]);
+      reinterpret_cast<uint2*>(to_v + 16)[kg >> 1] = make_uint2(x[2], x[3]);
     };
     channels(std::integral_constant<int, 0>{});
     if constexpr (C == 8) channels(std::integral_constant<int, 1>{});
   };
 
-  bf16x8_t qf[NT][KS][NP];
-  load_queries<D, NT, F32>(p, rw, kg, qf);
-  f32x4_t acc[NT][C], sa[NT][2];
-  Softmax<NT, C, NP> sm;
+  // queries: channels 16 s + 8 hh .. + 7 of the lane's row
+  bf16x8_t qf[QS][NP];
+#pragma unroll
+  for (int c = 0; c < QS; ++c)
+    load_query<F32>(p, rw.at[0] * p.q_stride + rw.head[0] * D + 16 * c + 8 * hh, rw.at[0] >= 0, qf[c]);
+  f32x16_t acc[CT], sa, sb;
+  float m = kLow, l = 0.f, raise = kLow;
   const float inv_c = 1.0f / p.c;
-  uint32_t poison = 0;
+  uint32_t poison = 0;  // bit b: a value of channel block b was NaN at a token that the lane's row attends to
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int c = 0; c < CT; ++c)
 #pragma unroll
-    for (int j = 0; j < C; ++j) acc[t][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto scores = [&](const Tile& from, f32x4_t (&s)[NT][2]) {
+    for (int i = 0; i < 16; ++i) acc[c][i] = 0.f;
+  auto scores = [&](const Tile& from, f32x16_t& s) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
     for (int kp = NP - 1; kp >= 0; --kp)  // small parts first
 #pragma unroll
-      for (int c = 0; c < KS; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bf16x8_t kf = __builtin_bit_cast(bf16x8_t, from.k[e][c][lane]);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) s[i][e] = mfma(kf, qf[i][c][kp], s[i][e]);
-        }
+      for (int c = 0; c < QS; ++c) s = mfma(__builtin_bit_cast(bf16x8_t, from.k[c][lane]), qf[c][kp], s);
   };
 
   Raw raw, ahead;  // codes of tile t + 2, and of t + 3 on their way
@@ -808,67 +810,85 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
       const int st[2] = {__builtin_amdgcn_readfirstlane(s0.x | s0.y), __builtin_amdgcn_readfirstlane(s1.x | s1.y)};
       const int have[2] = {st[0] & 255, st[1] & 255};
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) mask(sa[i][e], min(rw.lim[i] - t0 - 16 * e, have[e]) - 4 * kg);
+      for (int i = 0; i < 16; ++i) {
+        const int e = i / 8, tok = 8 * ((i / 4) & 1) + 4 * hh + i % 4;
+        sa[i] = tok < min(rw.lim[0] - t0 - 16 * e, have[e]) ? sa[i] : -INFINITY;
+      }
       if ((st[0] | st[1]) & 256)
         for (int e = 0; e < 2; ++e)
-          if (have[e] > 0)  // then its page is in the pool
-            mark_poison<D, NT>(head + table[t0 / KVTC_MX_PAGE + e] * page_bytes + R.kc + R.vc + R.sc + kg * (D / 32) * 4,
-                               t0 + 16 * e + 4 * kg, have[e] - 4 * kg, rw.lim, poison);
+          if (have[e] > 0) {  // then its page is in the pool
+            const uint8_t* vs = head + table[t0 / KVTC_MX_PAGE + e] * page_bytes + R.kc + R.vc + R.sc;
+            for (int g = hh; g < 4; g += 2)
+              mark_poison<D, 1>(vs + g * (D / 32) * 4, t0 + 16 * e + 4 * g, have[e] - 4 * g, rw.lim, poison);
+          }
     }
-    sm.vote(sa, p.c, inv_c, acc);
+    {  // one vote on whether a maximum has to move
+      const float mx = max2(max3(max3(sa[0], sa[1], sa[2]), max3(sa[3], sa[4], sa[5]), max3(sa[6], sa[7], sa[8])),
+                            max3(max3(sa[9], sa[10], sa[11]), max3(sa[12], sa[13], sa[14]), sa[15]));
+      if (__builtin_amdgcn_ballot_w64(mx > raise)) {
+        float x = mx * p.c;
+        x = fmaxf(x, __shfl_xor(x, 32));
+        const float nm = fmaxf(m, x), a = __builtin_amdgcn_exp2f(m - nm);
+        m = nm;
+        raise = (nm + kSlack) * inv_c;
+        l *= a;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[c] *= a;
+      }
+    }
     raw = ahead;
     clean(raw, t + 2, after);
     const int id = id_of(t + 3);
     __syncthreads();  // tile t + 1 is in its buffer, nobody reads tile t - 1 any more
     load_page(ahead, id);
     __builtin_amdgcn_sched_barrier(0);  // the loads first
-    f32x4_t sb[NT][2];
     scores(next, sb);
-    bf16x8_t pf[NT][NP];
-    sm.weights(sa, p.c, pf);
+    float w[16];
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, now.v[j][lane]);
+    for (int i = 0; i < 16; ++i) w[i] = __builtin_amdgcn_exp2f(__fmaf_rn(sa[i], p.c, -m));
+    l += (((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]))) +
+         (((w[8] + w[9]) + (w[10] + w[11])) + ((w[12] + w[13]) + (w[14] + w[15])));
+    bf16x8_t pf[2][NP];
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+    for (int u = 0; u < 2; ++u) {
+      float x[8];
 #pragma unroll
-        for (int kp = NP - 1; kp >= 0; --kp) acc[i][j] = mfma(vf, pf[i][kp], acc[i][j]);
+      for (int i = 0; i < 8; ++i) x[i] = w[8 * u + i];
+      split8<NP>(x, pf[u]);
     }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, now.v[u][c][lane]);
+#pragma unroll
+        for (int kp = NP - 1; kp >= 0; --kp) acc[c] = mfma(vf, pf[u][kp], acc[c]);
+      }
     convert(raw, after);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      sa[i][0] = sb[i][0];
-      sa[i][1] = sb[i][1];
-    }
+    sa = sb;
     b = b == 2 ? 0 : b + 1;
   }
 
-  // ---- a lane has channels [kg D / 4, (kg + 1) D / 4) of its row
+  // ---- a lane has channels C n .. of its row for the eight n = 8 a + 4 hh + i
+  l += __shfl_xor(l, 32);
+  poison |= (uint32_t)__shfl_xor((int)poison, 32);
+  if (rw.at[0] < 0) return;
+  const int64_t at = (int64_t)rw.at[0] * Hq + rw.head[0];
+  const int64_t slot = (int64_t)(p.slot0 + wk.split) * p.b.total_rows * Hq;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    float sum = sm.l[t];
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    uint32_t pz = poison >> (4 * t);
-    pz |= (uint32_t)__shfl_xor((int)pz, 16);
-    pz |= (uint32_t)__shfl_xor((int)pz, 32);
-    const bool dead = (pz >> (kg * (D / 32) / 4)) & 1u;
-    if (rw.at[t] < 0) continue;
-    const int64_t at = (int64_t)rw.at[t] * Hq + rw.head[t];
-    const int64_t slot = (int64_t)(p.slot0 + wk.split) * p.b.total_rows * Hq;
+  for (int a = 0; a < 2; ++a)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const int e = 8 * a + 4 * hh + i;
+      const bool dead = (poison >> (e * C / 32)) & 1u;
       float o[C];
 #pragma unroll
-      for (int j = 0; j < C; ++j) o[j] = dead ? NAN : acc[t][j][i];
-      store_row<F32>(p.ws_o ? p.ws_o + slot * D : nullptr, p.out, at, D, C * (4 * kg + i), o, sum);
+      for (int j = 0; j < C; ++j) o[j] = dead ? NAN : acc[j / 2][4 * (a + 2 * (j & 1)) + i];
+      store_row<F32>(p.ws_o ? p.ws_o + slot * D : nullptr, p.out, at, D, C * e, o, l);
     }
-    if (kg == 0) {
-      if (p.ws_o) p.ws_ml[slot + at] = make_float2(sm.m[t], sum);
-      else if (p.lse) p.lse[at] = log_sum(sm.m[t], sum);
-    }
+  if (hh == 0) {
+    if (p.ws_o) p.ws_ml[slot + at] = make_float2(m, l);
+    else if (p.lse) p.lse[at] = log_sum(m, l);
   }
 }
 

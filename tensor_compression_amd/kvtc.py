@@ -549,6 +549,11 @@ class Plan:
 
 # ---- microscaled paged cache (kvtc_mx_*)
 
+# The current stream's handle without the Stream object (2.6 us of a call that
+# a decode step makes for every layer).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 class MxBatch:
     """A ragged batch of sequences of an MxCache: device int32 arrays (kept
@@ -581,6 +586,7 @@ class MxCache:
         self._c = MxConfig(cfg["layers"], cfg["kv_heads"], cfg["head_dim"], cfg["dtype"], cfg["bits_k"],
                            cfg["bits_v"], pool_pages)
         self._ref = ctypes.byref(self._c)
+        self._lib = lib()
         rec, total = ctypes.c_size_t(0), ctypes.c_size_t(0)
         _check(lib().kvtc_mx_pool_size(self._ref, ctypes.byref(rec), ctypes.byref(total)), "kvtc_mx_pool_size")
         self.record_bytes, self.pool_bytes = rec.value, total.value
@@ -590,6 +596,8 @@ class MxCache:
         if pool.dtype != torch.uint8 or tuple(pool.shape) != shape or not pool.is_contiguous():
             raise ValueError(f"the pool is a contiguous uint8 tensor of shape {shape}")
         self.pool, self.pool_pages, self.device = pool, pool_pages, pool.device
+        self._index = pool.get_device()
+        self._strides = {}
         self.dtype = torch.float32 if cfg["dtype"] == FP32 else torch.bfloat16
         self._head = (cfg["kv_heads"], cfg["head_dim"])
         self._pool_ptr = pool.data_ptr()
@@ -601,45 +609,50 @@ class MxCache:
         return MxBatch(page_table, kv_lens, row_start, total_rows, max_rows, max_len)
 
     def _own(self, t):
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"a tensor on {t.device} for a cache on {self.device}")
 
     def _call(self, fn, stream, *args):
         """Runs a library call with the cache's device current."""
-        if torch.cuda.current_device() == self.device.index:
-            s = stream if stream is not None else torch.cuda.current_stream()
-            st = fn(*args, s.cuda_stream)
+        if torch.cuda.current_device() == self._index:
+            st = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(self._index))
         else:
-            with torch.cuda.device(self.device):
-                s = stream if stream is not None else torch.cuda.current_stream()
-                st = fn(*args, s.cuda_stream)
+            with torch.cuda.device(self._index):
+                st = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(self._index))
         if st != OK:
             raise KvtcError(st, fn.__name__)
 
     def _rows(self, x, batch, n_layers):
         """(pointer, strides) of a row tensor [rows, heads, head_dim] or
         [layers, heads, rows, head_dim]."""
-        if x.device != self.device:
-            self._own(x)
-        sh = x.shape
-        st = [t if d > 1 else 0 for t, d in zip(x.stride()[:-1], sh)] + [x.stride(-1)]
+        self._own(x)
+        sh, st = x.shape, x.stride()
+        H, D = self._head
         if len(sh) == 3:
-            ok = n_layers == 1 and sh == (batch.total_rows, *self._head)
-            strides = (0, st[1], st[0])
+            ok = n_layers == 1 and sh == (batch.total_rows, H, D)
+            key = (0, st[1], st[0])
         else:
-            ok = len(sh) == 4 and sh == (n_layers, self._head[0], batch.total_rows, self._head[1])
-            strides = st[:3] if ok else None
+            ok = len(sh) == 4 and sh == (n_layers, H, batch.total_rows, D)
+            key = st[:3]
         if not ok or st[-1] != 1:
             raise ValueError("rows are [total_rows, kv_heads, head_dim] of one layer or [layers, kv_heads, "
                              "total_rows, head_dim], with the channels contiguous")
-        return x.data_ptr(), (ctypes.c_int64 * 3)(*strides)
+        if 1 in sh:  # the stride of a single layer, head or row may be anything
+            one = (n_layers, H, batch.total_rows)
+            key = tuple(t if n > 1 else 0 for t, n in zip(key, one))
+        arr = self._strides.get(key)
+        if arr is None:  # conversions of stride triples, as they come up
+            if len(self._strides) > 256:
+                self._strides.clear()
+            arr = self._strides[key] = (ctypes.c_int64 * 3)(*key)
+        return x.data_ptr(), arr
 
     @staticmethod
     def _status(status):
         if status is None:
             return None
-        if status.dtype != torch.int32 or status.numel() < 1:
-            raise ValueError("status is an int32 tensor")
+        if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
+            raise ValueError("status is an int32 tensor on the device")
         return status.data_ptr()
 
     def write(self, batch: MxBatch, k: torch.Tensor, v: torch.Tensor, layer: int = 0,
@@ -650,7 +663,7 @@ class MxCache:
             raise ValueError(f"keys and values are {self.dtype}")
         n = k.shape[0] if k.dim() == 4 else 1
         (kp, ks), (vp, vs) = self._rows(k, batch, n), self._rows(v, batch, n)
-        self._call(lib().kvtc_mx_write, stream, self._ref, batch.ref, layer, n, kp, ks, vp, vs, self._pool_ptr,
+        self._call(self._lib.kvtc_mx_write, stream, self._ref, batch.ref, layer, n, kp, ks, vp, vs, self._pool_ptr,
                    self.pool_bytes, self._status(status))
 
     def read(self, batch: MxBatch, k_out: torch.Tensor, v_out: torch.Tensor, layer: int = 0,
@@ -661,7 +674,7 @@ class MxCache:
             raise ValueError("outputs are both bfloat16 or both float32")
         n = k_out.shape[0] if k_out.dim() == 4 else 1
         (kp, ks), (vp, vs) = self._rows(k_out, batch, n), self._rows(v_out, batch, n)
-        self._call(lib().kvtc_mx_read, stream, self._ref, batch.ref, layer, n, self._pool_ptr, self.pool_bytes, kp,
+        self._call(self._lib.kvtc_mx_read, stream, self._ref, batch.ref, layer, n, self._pool_ptr, self.pool_bytes, kp,
                    ks, vp, vs, BF16 if k_out.dtype == torch.bfloat16 else FP32, self._status(status))
         return k_out, v_out
 
@@ -673,34 +686,35 @@ class MxCache:
         return torch.empty(max(n.value, 16), dtype=torch.uint8, device=self.device)
 
     def _attention(self, batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream):
-        if q.device != self.device:
-            self._own(q)
-        heads, D = q.shape[1], self._head[1]
-        if q.dtype != self.dtype or q.dim() != 3 or q.shape[0] != batch.total_rows or q.shape[2] != D or \
-                q.stride(2) != 1 or (q.stride(1) != D and heads > 1):
+        self._own(q)
+        sh, st, D, index = q.shape, q.stride(), self._head[1], self._index
+        if q.dtype != self.dtype or len(sh) != 3 or sh[0] != batch.total_rows or sh[2] != D or st[2] != 1 or \
+                (st[1] != D and sh[1] > 1):
             raise ValueError(f"queries are {self.dtype} [total_rows, heads, {D}] with contiguous heads")
+        heads = sh[1]
         if out is None or ws is None:
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 if out is None:
-                    out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+                    out = torch.empty(sh, dtype=q.dtype, device=self.device)
                 if ws is None:
                     ws = self.workspace(batch, heads, shared_pages or 0)
-        if out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != self.device:
+        if out.dtype != q.dtype or out.shape != sh or not out.is_contiguous() or out.get_device() != index:
             raise ValueError("out is a contiguous tensor of the queries' type and shape")
         lp = None
         if lse is not None:
-            if lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or \
-                    lse.device != self.device:
+            if lse.dtype != torch.float32 or lse.shape != sh[:2] or not lse.is_contiguous() or \
+                    lse.get_device() != index:
                 raise ValueError("lse is a contiguous float32 tensor [total_rows, heads]")
             lp = lse.data_ptr()
-        if ws.device != self.device or not ws.is_contiguous():
+        if ws.get_device() != index or not ws.is_contiguous():
             raise ValueError("the workspace is a contiguous tensor on the cache's device")
-        tail = (q.data_ptr(), q.stride(0) if q.shape[0] > 1 else 0, heads, scale if scale is not None else D ** -0.5, 1 if causal else 0,
-                out.data_ptr(), lp, ws.data_ptr(), ws.nbytes, self._status(status))
+        tail = (q.data_ptr(), st[0] if sh[0] > 1 else 0, heads, scale if scale is not None else D ** -0.5,
+                1 if causal else 0, out.data_ptr(), lp, ws.data_ptr(), ws.nbytes, self._status(status))
         if shared_pages is None:
-            self._call(lib().kvtc_mx_attn, stream, self._ref, batch.ref, layer, self._pool_ptr, self.pool_bytes, *tail)
+            self._call(self._lib.kvtc_mx_attn, stream, self._ref, batch.ref, layer, self._pool_ptr, self.pool_bytes,
+                       *tail)
         else:
-            self._call(lib().kvtc_mx_attn_shared, stream, self._ref, batch.ref, layer, self._pool_ptr,
+            self._call(self._lib.kvtc_mx_attn_shared, stream, self._ref, batch.ref, layer, self._pool_ptr,
                        self.pool_bytes, shared_pages, *tail)
         return (out, lse) if lse is not None else out
 
