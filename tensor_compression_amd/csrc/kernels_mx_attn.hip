@@ -350,17 +350,20 @@ __device__ __forceinline__ float log_sum(float M, float L) {
 }
 
 // What a workgroup works on.  Heads vary fastest, so that (with 8 of them) a
-// head's tiles stay on one XCD and its pages in one L2; the last tiles,
-// longest when causal, come first.
+// head's tiles stay on one XCD and its pages in one L2.  The last tiles,
+// longest when causal, come first; where all workgroups are on the card at
+// once, two a CU, the second half goes the other way, so that a long tile
+// shares its CU with a short one.
 struct Work {
   int h, tile, split, z;
 };
-__device__ __forceinline__ Work work_of(const MxAttnParams& p) {
+__device__ __forceinline__ Work work_of(const MxAttnParams& p, int b) {
   Work w;
-  int b = blockIdx.x;
   w.h = b % p.H;
   b /= p.H;
-  w.tile = p.tiles - 1 - b % p.tiles;
+  w.tile = b % p.tiles;
+  if (!p.fold || 2 * w.tile < p.tiles) w.tile = p.tiles - 1 - w.tile;
+  else w.tile -= (p.tiles + 1) / 2;
   b /= p.tiles;
   w.split = b % p.nsplit;
   w.z = b / p.nsplit;
@@ -370,8 +373,13 @@ __device__ __forceinline__ Work work_of(const MxAttnParams& p) {
 // Few rows: memory bound, one pass over the codes with as many loads in
 // flight as the registers allow.  The waves take pairs of pages in turn, all
 // for the same 16 NT rows, and are joined at the end.
+template <int D>
+struct FewShared {
+  float o[4 * 16 * (D + 4)];
+  float2 ml[4][16];
+};
 template <int D, int BK, int BV, int NT, bool F32, bool ONCE>
-__global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const MxAttnParams p) {
+__device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewShared<D>& lds) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
   constexpr int C = D / 16;       // channels of an entry of the value groups
@@ -381,11 +389,8 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, kg = lane >> 4;
-  const Work wk = work_of(p);
+  const Work wk = work_of(p, block);
   const int h = wk.h;
-
-  __shared__ __attribute__((aligned(16))) float lds[4 * 16 * OS];
-  __shared__ float2 ml[4][16];
 
   const int Hq = p.H * p.G;
   MxSeq sq{0, 0, 0};
@@ -573,9 +578,9 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
       for (int j = 0; j < C; j += 4) {
         float4 o = make_float4(acc[t][j][i], acc[t][j + 1][i], acc[t][j + 2][i], acc[t][j + 3][i]);
         if (dead) o = make_float4(NAN, NAN, NAN, NAN);
-        *reinterpret_cast<float4*>(&lds[(wave * 16 + n) * OS + C * (4 * kg + i) + j]) = o;
+        *reinterpret_cast<float4*>(&lds.o[(wave * 16 + n) * OS + C * (4 * kg + i) + j]) = o;
       }
-    if (kg == 0) ml[wave][n] = make_float2(sm.m[t], sum);
+    if (kg == 0) lds.ml[wave][n] = make_float2(sm.m[t], sum);
     const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
     const int row = __shfl(rw.at[t], r), hq = __shfl(rw.head[t], r);
     __syncthreads();
@@ -583,11 +588,11 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
     const int64_t at = (int64_t)row * Hq + hq;
     float M = kLow, L = 0.f, a[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[w][r].x);
+    for (int w = 0; w < 4; ++w) M = fmaxf(M, lds.ml[w][r].x);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      a[w] = __builtin_amdgcn_exp2f(ml[w][r].x - M);
-      L = __fmaf_rn(a[w], ml[w][r].y, L);
+      a[w] = __builtin_amdgcn_exp2f(lds.ml[w][r].x - M);
+      L = __fmaf_rn(a[w], lds.ml[w][r].y, L);
     }
     float o[C];
 #pragma unroll
@@ -595,7 +600,7 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(&lds[(w * 16 + r) * OS + c0 + j]);
+        const float4 x = *reinterpret_cast<const float4*>(&lds.o[(w * 16 + r) * OS + c0 + j]);
         s.x = __fmaf_rn(a[w], x.x, s.x);
         s.y = __fmaf_rn(a[w], x.y, s.y);
         s.z = __fmaf_rn(a[w], x.z, s.z);
@@ -615,6 +620,12 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
   }
 }
 
+template <int D, int BK, int BV, int NT, bool F32, bool ONCE>
+__global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const MxAttnParams p) {
+  __shared__ __attribute__((aligned(16))) FewShared<D> lds;
+  few_rows<D, BK, BV, NT, F32, ONCE>(p, blockIdx.x, lds);
+}
+
 // Many rows: bound by the issue of matrix and vector instructions.  A
 // workgroup takes 128 rows, 32 a wave, and walks over the tokens 32 at a
 // time; each wave turns half of a page into operands in LDS, in the order in
@@ -629,64 +640,48 @@ __global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const 
 // the slice of P^T that the product with 16 tokens' values takes from it.
 // Value rows of a 32-channel product: row n + 16 o is channel 2 ct + o of
 // entry n of the value groups.
+template <int D>
+struct ManyShared {
+  struct Tile {
+    uint4 k[D / 16][64];     // contraction step, operand lane
+    uint4 v[2][D / 32][64];  // page, channel tile, operand lane
+    int2 state[2];           // per page and half: tokens that exist, bit 8 if a NaN value was taken out
+  } tile[3];
+  int2 bounds[4];
+  int odd[4];  // per wave: it met a page outside the pool, so every tile's state is looked at
+};
 template <int D, int BK, int BV, bool F32>
-__global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
+__device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, ManyShared<D>& lds) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
   constexpr int C = D / 16, KS = D / 32, QS = D / 16, CT = D / 32, NP = F32 ? 3 : 1;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, kg = lane >> 4, hh = lane >> 5;
-  const Work wk = work_of(p);
+  using Tile = typename ManyShared<D>::Tile;
+  Tile(&tile)[3] = lds.tile;
+  const Work wk = work_of(p, block);
   const int h = wk.h;
-
-  struct Tile {
-    uint4 k[QS][64];      // contraction step, operand lane
-    uint4 v[2][CT][64];   // page, channel tile, operand lane
-    int2 state[2];        // per page and half: tokens that exist, bit 8 if a NaN value was taken out
-  };
-  __shared__ Tile tile[3];
-  __shared__ int2 bounds[4];
-  __shared__ int odd;  // a page outside the pool was met: every tile's state is looked at
 
   const int Hq = p.H * p.G;
   MxSeq sq{0, 0, 0};
   if (!p.prefix) sq = mx_seq(p.b, wk.z, p.status);
   const int rows = (p.prefix ? p.b.total_rows : sq.n) * p.G;
   if (wk.tile * 128 >= rows) return;
-  Rows<1> rw = rows_of<1>(p, sq, h, wk.tile * 128 + wave * 32, rows, lane & 31);
-  {  // rows_of looks at the first 16 lanes
-    const int lo = rw.at[0] >= 0 ? rw.lim[0] : 0x7FFFFFFF;
-    rw.lo = min(rw.lo, __builtin_amdgcn_readlane(row_min(lo), 16));
-    rw.hi = max(rw.hi, __builtin_amdgcn_readlane(row_max(rw.lim[0]), 16));
-  }
-  if (lane == 0) bounds[wave] = make_int2(rw.lo, rw.hi);
-  if (threadIdx.x == 0) odd = 0;
-  __syncthreads();
-  int lo = 0x7FFFFFFF, hi = 0;  // of all four waves
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    lo = min(lo, bounds[w].x);
-    hi = max(hi, bounds[w].y);
-  }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
   const int begin = p.begin + wk.split * p.chunk;
-  const int end = min(min(p.end, begin + p.chunk), hi);
-  if (p.ws_o && begin >= end) return;
+  int end = min(begin + p.chunk, p.prefix ? p.end : sq.len);
 
+  // This wave converts half `half` (of a lane's key channels and of the value
+  // channel pairs) of page p0 + 2 t + own of tile t: the numbers of 64 tiles,
+  // one a lane, the next 64 on their way; -1 as in few_rows.  They and the
+  // first pages are asked for before the rows are looked up.
   const int32_t* table = p.b.page_table + (p.prefix ? 0 : (int64_t)wk.z * p.b.max_pages);
   const uint8_t* head = p.pool + (int64_t)h * R.bytes;
   const int64_t page_bytes = (int64_t)p.H * R.bytes;
   const Sh sh(n, kg);
   const int p0 = begin / KVTC_MX_PAGE, p1 = (end + KVTC_MX_PAGE - 1) / KVTC_MX_PAGE;
-  const int tiles = (p1 - p0 + 1) / 2;
-
-  // This wave converts half `half` (of a lane's key channels and of the value
-  // channel pairs) of page p0 + 2 t + own of tile t: the numbers of 64 tiles,
-  // one a lane, the next 64 on their way; -1 as in k_mx_attn.
   const int own = wave & 1, half = wave >> 1;
-  auto load_ids = [&](int t) {
+  auto load_ids = [&](int t, bool& bad) {
     const int pg = p0 + (t + lane) * 2 + own;
     int id = -1;
     if (pg < p1) {
@@ -694,16 +689,23 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
       if ((uint32_t)id >= (uint32_t)p.pool_pages) {
         if (p.status) atomicOr(p.status, 1u << KVTC_ERR_INVALID_ARG);
         id = -1;
-        odd = 1;
+        bad = true;
       }
     }
     return id;
   };
-  int ids = load_ids(0), ids2 = load_ids(64);
+  bool bad = false;
+  int ids = load_ids(0, bad), ids2 = load_ids(64, bad);
+  {
+    const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
+    if (lane == 0) lds.odd[wave] = any != 0;
+  }
   auto id_of = [&](int t) {  // called for every t in turn
     if (t && (t & 63) == 0) {
       ids = ids2;
-      ids2 = load_ids(t + 64);
+      bool more = false;
+      ids2 = load_ids(t + 64, more);
+      if (more) lds.odd[wave] = 1;
     }
     return __builtin_amdgcn_readlane(ids, t & 63);
   };
@@ -719,7 +721,37 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
     g.ks = rec[sh.ks];
     g.vs = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
   };
-  // what must not reach the products, as in k_mx_attn; each wave marks its own rows
+  // Codes of tile t in raw[t % 3]: those of tile t + 2 are converted while
+  // those of t + 3 and t + 4 are on their way (2000 clocks from the request on).
+  Raw raw[3];
+#pragma unroll
+  for (int t = 0; t < 3; ++t) load_page(raw[t], id_of(t));
+
+  Rows<1> rw = rows_of<1>(p, sq, h, wk.tile * 128 + wave * 32, rows, lane & 31);
+  {  // rows_of looks at the first 16 lanes
+    const int lo = rw.at[0] >= 0 ? rw.lim[0] : 0x7FFFFFFF;
+    rw.lo = min(rw.lo, __builtin_amdgcn_readlane(row_min(lo), 16));
+    rw.hi = max(rw.hi, __builtin_amdgcn_readlane(row_max(rw.lim[0]), 16));
+  }
+  // queries: channels 16 s + 8 hh .. + 7 of the lane's row
+  bf16x8_t qf[QS][NP];
+#pragma unroll
+  for (int c = 0; c < QS; ++c)
+    load_query<F32>(p, rw.at[0] * p.q_stride + rw.head[0] * D + 16 * c + 8 * hh, rw.at[0] >= 0, qf[c]);
+  if (lane == 0) lds.bounds[wave] = make_int2(rw.lo, rw.hi);
+  __syncthreads();
+  int lo = 0x7FFFFFFF, hi = 0;  // of all four waves
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    lo = min(lo, lds.bounds[w].x);
+    hi = max(hi, lds.bounds[w].y);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  end = min(end, __builtin_amdgcn_readfirstlane(hi));
+  if (p.ws_o && begin >= end) return;
+  const int tiles = (end - p0 * KVTC_MX_PAGE + 31) / 32;
+
+  // what must not reach the products, as in few_rows; each wave marks its own rows
   auto clean = [&](Raw& g, int t, Tile& to) {
     const int t0 = (p0 + 2 * t + own) * KVTC_MX_PAGE;
     const int have = g.id < 0 ? 0 : min(max(end - t0, 0), 16);
@@ -764,12 +796,7 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
     if constexpr (C == 8) channels(std::integral_constant<int, 1>{});
   };
 
-  // queries: channels 16 s + 8 hh .. + 7 of the lane's row
-  bf16x8_t qf[QS][NP];
-#pragma unroll
-  for (int c = 0; c < QS; ++c)
-    load_query<F32>(p, rw.at[0] * p.q_stride + rw.head[0] * D + 16 * c + 8 * hh, rw.at[0] >= 0, qf[c]);
-  f32x16_t acc[CT], sa, sb;
+  f32x16_t acc[CT], sa;
   float m = kLow, l = 0.f, raise = kLow;
   const float inv_c = 1.0f / p.c;
   uint32_t poison = 0;  // bit b: a value of channel block b was NaN at a token that the lane's row attends to
@@ -786,25 +813,24 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
       for (int c = 0; c < QS; ++c) s = mfma(__builtin_bit_cast(bf16x8_t, from.k[c][lane]), qf[c][kp], s);
   };
 
-  Raw raw, ahead;  // codes of tile t + 2, and of t + 3 on their way
   if (tiles > 0) {
-    load_page(raw, id_of(0));
-    load_page(ahead, id_of(1));
-    clean(raw, 0, tile[0]);
-    convert(raw, tile[0]);
-    load_page(raw, id_of(2));
-    clean(ahead, 1, tile[1]);
-    convert(ahead, tile[1]);
-    ahead = raw;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      clean(raw[t], t, tile[t]);
+      convert(raw[t], tile[t]);
+    }
+    load_page(raw[0], id_of(3));
     __syncthreads();
     scores(tile[0], sa);
   }
-  int b = 0, slow = 0;  // buffer of tile t
-  for (int t = 0; t < tiles; ++t) {
-    Tile &now = tile[b], &next = tile[b == 2 ? 0 : b + 1], &after = tile[b == 0 ? 2 : b - 1];
+  int slow = 0;
+  auto step = [&](int t, auto bc) {
+    constexpr int b = decltype(bc)::value;  // t % 3
+    Tile &now = tile[b], &next = tile[(b + 1) % 3], &after = tile[(b + 2) % 3];
+    Raw &use = raw[(b + 2) % 3], &load = raw[(b + 1) % 3];
     const int t0 = (p0 + 2 * t) * KVTC_MX_PAGE;
     // the page numbers of tile t were read at least 64 tiles, or the opening barrier, ago
-    if ((t & 63) == 0) slow = __builtin_amdgcn_readfirstlane(odd);
+    if ((t & 63) == 0) slow = __builtin_amdgcn_readfirstlane(lds.odd[0] | lds.odd[1] | lds.odd[2] | lds.odd[3]);
     if (slow || t0 + 32 > min(end, rw.lo)) {
       const int2 s0 = now.state[0], s1 = now.state[1];
       const int st[2] = {__builtin_amdgcn_readfirstlane(s0.x | s0.y), __builtin_amdgcn_readfirstlane(s1.x | s1.y)};
@@ -836,16 +862,18 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
         for (int c = 0; c < CT; ++c) acc[c] *= a;
       }
     }
-    raw = ahead;
-    clean(raw, t + 2, after);
-    const int id = id_of(t + 3);
+    clean(use, t + 2, after);
+    const int id = id_of(t + 4);
     __syncthreads();  // tile t + 1 is in its buffer, nobody reads tile t - 1 any more
-    load_page(ahead, id);
+    load_page(load, id);
     __builtin_amdgcn_sched_barrier(0);  // the loads first
-    scores(next, sb);
+    __builtin_amdgcn_s_setprio(1);
     float w[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __builtin_amdgcn_exp2f(__fmaf_rn(sa[i], p.c, -m));
+    for (int i = 0; i < 16; ++i) w[i] = __fmaf_rn(sa[i], p.c, -m);
+    scores(next, sa);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __builtin_amdgcn_exp2f(w[i]);
     l += (((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]))) +
          (((w[8] + w[9]) + (w[10] + w[11])) + ((w[12] + w[13]) + (w[14] + w[15])));
     bf16x8_t pf[2][NP];
@@ -864,9 +892,13 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
 #pragma unroll
         for (int kp = NP - 1; kp >= 0; --kp) acc[c] = mfma(vf, pf[u][kp], acc[c]);
       }
-    convert(raw, after);
-    sa = sb;
-    b = b == 2 ? 0 : b + 1;
+    convert(use, after);
+    __builtin_amdgcn_s_setprio(0);
+  };
+  for (int t = 0; t < tiles; t += 3) {
+    step(t, std::integral_constant<int, 0>{});
+    if (t + 1 < tiles) step(t + 1, std::integral_constant<int, 1>{});
+    if (t + 2 < tiles) step(t + 2, std::integral_constant<int, 2>{});
   }
 
   // ---- a lane has channels C n .. of its row for the eight n = 8 a + 4 hh + i
@@ -890,6 +922,25 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
     if (p.ws_o) p.ws_ml[slot + at] = make_float2(m, l);
     else if (p.lse) p.lse[at] = log_sum(m, l);
   }
+}
+
+template <int D, int BK, int BV, bool F32>
+__global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
+  __shared__ __attribute__((aligned(16))) ManyShared<D> lds;
+  many_rows<D, BK, BV, F32>(p, blockIdx.x, lds);
+}
+
+// A decode step behind a shared prefix: the prefix for all rows together and
+// each sequence's own tokens in one launch (one after the other they would
+// leave the card half empty twice).
+template <int D, int BK, int BV, bool F32>
+__global__ __launch_bounds__(256, 2) void k_mx_both(const MxAttnParams prefix, const MxAttnParams own, int prefix_blocks) {
+  __shared__ __attribute__((aligned(16))) union {
+    ManyShared<D> many;
+    FewShared<D> few;
+  } lds;
+  if ((int)blockIdx.x < prefix_blocks) many_rows<D, BK, BV, F32>(prefix, blockIdx.x, lds.many);
+  else few_rows<D, BK, BV, 1, F32, false>(own, (int)blockIdx.x - prefix_blocks, lds.few);
 }
 
 // Joins a row's partials: W waves a (row, head), sixteen lanes on its
@@ -966,30 +1017,44 @@ __global__ __launch_bounds__(256) void k_mx_join(const MxJoinParams p) {
   if (p.lse && c0 == 0) p.lse[at] = log_sum(M, L);
 }
 
+unsigned blocks_of(const MxAttnParams& p) {
+  return (unsigned)p.H * p.tiles * p.nsplit * (p.prefix ? 1 : p.b.n_seqs);
+}
 template <int D, int BK, int BV, bool F32>
-void launch_format(const MxAttnParams& p, unsigned grid, hipStream_t s) {
+void launch_pass(const MxAttnParams& p, hipStream_t s) {
+  const unsigned grid = blocks_of(p);
   if (p.nt == 1) {
     if (p.once) k_mx_attn<D, BK, BV, 1, F32, true><<<grid, 256, 0, s>>>(p);
     else k_mx_attn<D, BK, BV, 1, F32, false><<<grid, 256, 0, s>>>(p);
   } else if (p.nt == 2) k_mx_attn<D, BK, BV, 2, F32, false><<<grid, 256, 0, s>>>(p);
   else k_mx_rows<D, BK, BV, F32><<<grid, 256, 0, s>>>(p);
 }
-template <int D, int BK, int BV>
-hipError_t launch_attn(const MxAttnParams& p, bool f32, hipStream_t s) {
-  const unsigned grid = (unsigned)p.H * p.tiles * p.nsplit * (p.prefix ? 1 : p.b.n_seqs);
-  f32 ? launch_format<D, BK, BV, true>(p, grid, s) : launch_format<D, BK, BV, false>(p, grid, s);
+template <int D, int BK, int BV, bool F32>
+hipError_t launch_format(const MxAttnParams* prefix, const MxAttnParams* own, hipStream_t s) {
+  if (prefix && own && prefix->nt == 8 && own->nt == 1 && !own->once) {
+    const unsigned n = blocks_of(*prefix);
+    k_mx_both<D, BK, BV, F32><<<n + blocks_of(*own), 256, 0, s>>>(*prefix, *own, (int)n);
+    return hipGetLastError();
+  }
+  if (prefix) launch_pass<D, BK, BV, F32>(*prefix, s);
+  if (own) launch_pass<D, BK, BV, F32>(*own, s);
   return hipGetLastError();
+}
+template <int D, int BK, int BV>
+hipError_t launch_attn(const MxAttnParams* prefix, const MxAttnParams* own, bool f32, hipStream_t s) {
+  return f32 ? launch_format<D, BK, BV, true>(prefix, own, s) : launch_format<D, BK, BV, false>(prefix, own, s);
 }
 
 }  // namespace
 
-hipError_t launch_mx_attn(const MxAttnParams& p, int D, int bk, int bv, bool f32, hipStream_t s) {
+hipError_t launch_mx_attn(const MxAttnParams* prefix, const MxAttnParams* own, int D, int bk, int bv, bool f32,
+                          hipStream_t s) {
   if (D == 128) {
-    if (bk == 4) return bv == 4 ? launch_attn<128, 4, 4>(p, f32, s) : launch_attn<128, 4, 8>(p, f32, s);
-    return bv == 4 ? launch_attn<128, 8, 4>(p, f32, s) : launch_attn<128, 8, 8>(p, f32, s);
+    if (bk == 4) return bv == 4 ? launch_attn<128, 4, 4>(prefix, own, f32, s) : launch_attn<128, 4, 8>(prefix, own, f32, s);
+    return bv == 4 ? launch_attn<128, 8, 4>(prefix, own, f32, s) : launch_attn<128, 8, 8>(prefix, own, f32, s);
   }
-  if (bk == 4) return bv == 4 ? launch_attn<64, 4, 4>(p, f32, s) : launch_attn<64, 4, 8>(p, f32, s);
-  return bv == 4 ? launch_attn<64, 8, 4>(p, f32, s) : launch_attn<64, 8, 8>(p, f32, s);
+  if (bk == 4) return bv == 4 ? launch_attn<64, 4, 4>(prefix, own, f32, s) : launch_attn<64, 4, 8>(prefix, own, f32, s);
+  return bv == 4 ? launch_attn<64, 8, 4>(prefix, own, f32, s) : launch_attn<64, 8, 8>(prefix, own, f32, s);
 }
 
 template <int D, bool F32>

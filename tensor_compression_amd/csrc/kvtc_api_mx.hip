@@ -197,26 +197,28 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
     p.ws_o = (float*)ws;
     p.ws_ml = (float2*)(p.ws_o + a.slots * b->total_rows * q_heads * (int64_t)cfg->head_dim);
   }
-  auto pass = [&](const Cut& c) {
+  auto cut = [&](const Cut& c) {
+    p.nt = c.nt;
     p.tiles = (int32_t)c.tiles;
     p.nsplit = c.nsplit;
     p.chunk = c.chunk;
-    p.nt = c.nt;
-    return launch_mx_attn(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, f32, stream);
   };
-  if (a.prefix.nsplit) {
-    p.prefix = 1;
-    p.end = a.begin;
-    if (pass(a.prefix) != hipSuccess) return KVTC_ERR_HIP;
-    p.prefix = 0;
-  }
-  // at most this many bytes of codes, against the 256 MB of the memory-side cache
-  p.once = (int64_t)b->n_seqs * (b->max_len - a.begin) / KVTC_MX_PAGE * cfg->kv_heads *
-               mx_record(cfg->head_dim, cfg->bits_k, cfg->bits_v).bytes > ((int64_t)256 << 20);
+  cut(a.prefix);
+  p.prefix = 1;
+  p.end = a.begin;
+  const MxAttnParams prefix = p;
+  cut(a.own);
+  p.prefix = 0;
   p.begin = a.begin;
   p.end = 0x7FFFFFFF;
   p.slot0 = a.prefix.nsplit;
-  if (a.own.nsplit && pass(a.own) != hipSuccess) return KVTC_ERR_HIP;
+  p.fold = causal && a.own.nt == 8 && a.own.tiles * cfg->kv_heads * a.own.nsplit * b->n_seqs <= 512;
+  // at most this many bytes of codes, against the 256 MB of the memory-side cache
+  p.once = (int64_t)b->n_seqs * (b->max_len - a.begin) / KVTC_MX_PAGE * cfg->kv_heads *
+               mx_record(cfg->head_dim, cfg->bits_k, cfg->bits_v).bytes > ((int64_t)256 << 20);
+  if (launch_mx_attn(a.prefix.nsplit ? &prefix : nullptr, a.own.nsplit ? &p : nullptr, cfg->head_dim, cfg->bits_k,
+                     cfg->bits_v, f32, stream) != hipSuccess)
+    return KVTC_ERR_HIP;
   if (!a.slots) return KVTC_OK;
   MxJoinParams j{};
   j.b = *b;

@@ -43,6 +43,7 @@ struct MxAttnParams {
   int32_t prefix;      // 1: rows of all sequences against the first one's pages
   int32_t begin, end;  // token range of this pass
   int32_t nt;    // 16-row tiles of a workgroup: 1 or 2 (k_mx_attn), 8 (k_mx_rows)
+  int32_t fold;  // pair long tiles with short ones
   int32_t once;  // read the codes past the caches (nt 1)
   int32_t tiles, nsplit, chunk;
   int32_t slot0;   // first partial slot of this pass
@@ -66,7 +67,9 @@ struct MxJoinParams {
 
 hipError_t launch_mx_write(const MxIoParams& p, int D, int bk, int bv, bool f32, hipStream_t s);
 hipError_t launch_mx_read(const MxIoParams& p, int D, int bk, int bv, bool f32, hipStream_t s);
-hipError_t launch_mx_attn(const MxAttnParams& p, int D, int bk, int bv, bool f32, hipStream_t s);
+// The passes of a call (either may be null), both before the join.
+hipError_t launch_mx_attn(const MxAttnParams* prefix, const MxAttnParams* own, int D, int bk, int bv, bool f32,
+                          hipStream_t s);
 hipError_t launch_mx_join(const MxJoinParams& p, bool f32, hipStream_t s);
 
 #if defined(__HIPCC__)
