@@ -126,11 +126,14 @@ Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span) {
   c.tiles = (rows + 16 * c.nt - 1) / (16 * c.nt);
   // As many workgroups as the card takes at its rate: one a CU for few rows
   // (1 sequence of 131072 tokens: 41 us with 256, 42 with 768, and more
-  // partials to join), two for many rows, which need the second's waves.
-  // Short sequences stay whole: a step of 128 tokens costs 0.55 us, a second
-  // launch and its join 2.8 us.
+  // partials to join), two for many rows, which need the second's waves (128
+  // sequences behind 32768 tokens: 220 us with 256, 166 with 512) unless
+  // that left them less than 512 tokens each (64 behind 8192: 41 and 52 us).
+  // Sequences of few rows stay whole up to 640 tokens: a step of 128 tokens
+  // costs 0.55 us, a second launch and its join 2.8 us.
   const int64_t units = c.tiles * H * seqs, room = c.nt == 8 ? 512 : 256;
-  const int64_t n = span <= 640 ? 1 : std::max<int64_t>(1, std::min(room / units, (span + 127) / 128));
+  const int64_t most = c.nt == 8 ? span / 512 : span <= 640 ? 1 : (span + 127) / 128;
+  const int64_t n = std::max<int64_t>(1, std::min(room / units, most));
   c.chunk = (int)(((span + n - 1) / n + 127) / 128 * 128);
   c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / std::max(c.chunk, 1));
   return c;
