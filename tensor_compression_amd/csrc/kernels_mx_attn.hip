@@ -831,7 +831,8 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
     const int t0 = (p0 + 2 * t) * KVTC_MX_PAGE;
     // the page numbers of tile t were read at least 64 tiles, or the opening barrier, ago
     if ((t & 63) == 0) slow = __builtin_amdgcn_readfirstlane(lds.odd[0] | lds.odd[1] | lds.odd[2] | lds.odd[3]);
-    if (slow || t0 + 32 > min(end, rw.lo)) {
+    // (by the bound of all four waves: `clean` may have taken a NaN out that this wave's rows attend to)
+    if (slow || t0 + 32 > min(end, lo)) {
       const int2 s0 = now.state[0], s1 = now.state[1];
       const int st[2] = {__builtin_amdgcn_readfirstlane(s0.x | s0.y), __builtin_amdgcn_readfirstlane(s1.x | s1.y)};
       const int have[2] = {st[0] & 255, st[1] & 255};

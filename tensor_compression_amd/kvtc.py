@@ -567,6 +567,7 @@ class MxBatch:
             if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError("page_table [n, pages], kv_lens [n] and row_start [n + 1] are contiguous int32")
         self.page_table, self.kv_lens, self.row_start = page_table, kv_lens, row_start
+        self.index = page_table.get_device()
         self.total_rows, self.max_rows, self.max_len = total_rows, max_rows, max_len
         self._c = MxBatchStruct(n, page_table.shape[1], total_rows, max_rows, max_len, 0, page_table.data_ptr(),
                                 kv_lens.data_ptr(), row_start.data_ptr())
@@ -626,6 +627,8 @@ class MxCache:
         """(pointer, strides) of a row tensor [rows, heads, head_dim] or
         [layers, heads, rows, head_dim]."""
         self._own(x)
+        if batch.index != self._index:
+            raise ValueError("a batch on another device than the cache")
         sh, st = x.shape, x.stride()
         H, D = self._head
         if len(sh) == 3:
@@ -687,6 +690,8 @@ class MxCache:
 
     def _attention(self, batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream):
         self._own(q)
+        if batch.index != self._index:
+            raise ValueError("a batch on another device than the cache")
         sh, st, D, index = q.shape, q.stride(), self._head[1], self._index
         if q.dtype != self.dtype or len(sh) != 3 or sh[0] != batch.total_rows or sh[2] != D or st[2] != 1 or \
                 (st[1] != D and sh[1] > 1):

@@ -290,6 +290,23 @@ def test_attention_shared_prefix(shared, dtype):
             assert torch.equal(out, out2) and c.status.item() == 0
 
 
+def test_attention_with_nothing_but_the_prefix():
+    """Every sequence inside the prefix, whose last page is not full; and
+    sequences without any token."""
+    for G in (2, 40):
+        c = Case(128, 8, 4, kvtc.BF16, 2, [1, 2, 1], [37, 20, 0], seed=G, shared=3)
+        one = c.cache.batch(c.table_dev[:1], dev([37], torch.int32), dev([0, 37], torch.int32), total_rows=37, max_rows=37,
+                            max_len=37)
+        c.cache.write(one, c.rand(37, 2, 128), c.rand(37, 2, 128))
+        q, out, lse, scale = run_attention(c, G, shared=3)
+        check_attention(c, q, out, lse, scale, True, f"only prefix G{G}")
+    for shared in (None, 3):
+        c.batch = c.new_batch([1, 2, 1], [0, 0, 0])
+        c.lens = [0, 0, 0]
+        q, out, lse, scale = run_attention(c, 40, shared=shared)
+        assert not out.any() and torch.isneginf(lse).all()
+
+
 def test_attention_shared_prefix_many_rows():
     """Enough rows together for whole 64-row tiles of the prefix pass."""
     lens = [160 + int(x) for x in np.random.default_rng(1).integers(0, 90, 70)]
@@ -341,11 +358,14 @@ def test_attention_scales(scale):
         check_attention(c, q, out, lse, scale, True, f"ramp {sign} scale {scale}")
 
 
+@pytest.mark.parametrize("rows", [3, 20, 80])
 @pytest.mark.parametrize("D,bv", [(64, 4), (64, 8), (128, 4), (128, 8)])
 @pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
-def test_nan_tokens_reach_only_rows_that_attend_to_them(D, bv, dtype):
-    rows, ln, H, G = 20, 100, 2, 2
-    for kv, pos in ((0, 90), (1, 90), (1, 99), (1, 81), (0, 99)):
+def test_nan_tokens_reach_only_rows_that_attend_to_them(D, bv, dtype, rows):
+    """Few, some and many rows (a kernel each)."""
+    ln, H, G = rows + 80, 2, 2
+    for kv, back in ((0, 2), (1, 2), (1, 1), (1, rows - 1), (0, 1), (1, rows + 40)):
+        pos = ln - back
         c = Case(D, 8, bv, dtype, H, [rows], [ln], seed=pos)
         k, v = c.rand(ln, H, D), c.rand(ln, H, D)
         (k, v)[kv][pos, 1, 33] = float("nan")
@@ -354,35 +374,39 @@ def test_nan_tokens_reach_only_rows_that_attend_to_them(D, bv, dtype):
         q = c.rand(rows, H * G, D)
         out = c.cache.attention(c.batch, q)
         want = torch.zeros(rows, H * G, D, dtype=torch.bool, device="cuda")
-        first = pos - (ln - rows)
+        first = max(pos - (ln - rows), 0)
         want[first:, G:, :] = kv == 0
         want[first:, G:, 32:64] = True
         assert torch.equal(torch.isnan(out), want), (kv, pos)
     # as a query: its own row and head only
-    q[3, 1, 5] = float("nan")
+    q[2, 1, 5] = float("nan")
     want = torch.isnan(out)
     out2 = c.cache.attention(c.batch, q)
-    want[3, 1] = True
+    want[2, 1] = True
     assert torch.equal(torch.isnan(out2), want)
 
 
-def test_nan_tokens_in_the_prefix_pass():
-    """A sequence inside the prefix does not see the NaN that the others see."""
-    c = Case(128, 4, 4, kvtc.BF16, 1, [1, 1, 1], [32, 20, 40], shared=2, seed=4)
-    k, v = c.rand(92, 1, 128), c.rand(92, 1, 128)
-    k[32:52], v[32:52] = k[:20], v[:20]
-    k[52:84], v[52:84] = k[:32], v[:32]
-    for x in (0, 52):
-        v[x + 25, 0, 100] = float("nan")
-    b = c.cache.batch(c.table_dev, dev(c.lens, torch.int32), dev([0, 32, 52, 92], torch.int32), total_rows=92,
-                      max_rows=40, max_len=40)
-    c.cache.write(b, k, v)
-    q = c.rand(3, 2, 128)
-    nan = torch.isnan(c.cache.attention_shared(c.batch, q, 2))
+@pytest.mark.parametrize("n", [3, 40])
+def test_nan_token_in_the_prefix(n):
+    """A sequence inside the prefix does not see the NaN that the others see,
+    with few rows together and with many."""
+    lens = [32 + 7 * (z % 3) if z % 4 else 20 for z in range(n)]
+    lens[0] = 32
+    c = Case(128, 4, 4, kvtc.BF16, 1, [1] * n, lens, shared=2, seed=n)
+    first = c.cache.batch(c.table_dev[:1], dev([32], torch.int32), dev([0, 32], torch.int32), total_rows=32, max_rows=32,
+                          max_len=32)
+    k, v = c.rand(32, 1, 128), c.rand(32, 1, 128)
+    v[25, 0, 100] = float("nan")
+    c.cache.write(first, k, v)
+    rest = [max(x - 32, 0) for x in lens]
+    own = c.cache.batch(c.table_dev, dev(lens, torch.int32), dev([0] + [int(x) for x in np.cumsum(rest)], torch.int32),
+                        total_rows=max(sum(rest), 1), max_rows=max(max(rest), 1), max_len=max(lens))
+    c.cache.write(own, c.rand(max(sum(rest), 1), 1, 128), c.rand(max(sum(rest), 1), 1, 128), status=c.status)
+    q = c.rand(n, 2, 128)
+    nan = torch.isnan(c.cache.attention_shared(c.batch, q, 2, status=c.status))
     want = torch.zeros_like(nan)
-    want[0, :, 96:] = True
-    want[2, :, 96:] = True
-    assert torch.equal(nan, want)
+    want[[z for z in range(n) if lens[z] > 25], :, 96:] = True
+    assert torch.equal(nan, want) and c.status.item() == 0
 
 
 def test_attention_infinite_query():
@@ -455,6 +479,47 @@ def test_bad_metadata_is_reported_and_skipped():
     c, q, good = fresh()
     c.cache.attention(c.batch, q, status=c.status)
     assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("rows,page", [(2, 5), (2, 150), (40, 60), (200, 0), (200, 100), (200, 180)])
+def test_pages_outside_the_pool_anywhere(rows, page):
+    """Near the start and far behind it, for few, some and many rows: exactly
+    that page's tokens are missing."""
+    H, G, D, ln = 1, 1 if rows > 2 else 2, 64, 3000
+    c = Case(D, 8, 8, kvtc.FP32, H, [rows], [ln], seed=rows + page)
+    c.fill()
+    q = c.rand(rows, H * G, D)
+    c.table_dev[0, page] = c.pages + 3
+    out = c.cache.attention(c.batch, q, status=c.status)
+    assert c.status.item() == 1 << kvtc.ERR_INVALID_ARG
+    kp, vp = c.unpacked()
+    k, v = mx_ref.tokens(kp, vp, c.table[0], ln)
+    keep = np.arange(ln) // 16 != page
+    for r in (0, rows // 2, rows - 1):
+        lim = ln - rows + r + 1
+        m = keep[:lim]
+        s = D ** -0.5 * (k[0, :lim][m] @ np64(q)[r].T)
+        p = np.exp(s - s.max(0))
+        want = (p / p.sum(0)).T @ v[0, :lim][m]
+        assert np.abs(np64(out)[r] - want).max() < 1e-5 * np.abs(v[0, :lim][m]).max()
+
+
+def test_loose_bounds_give_the_same():
+    """Bounds far above what the device arrays hold (a captured step's) choose
+    other kernels and other splits, not other results."""
+    rows, lens = [1, 2, 1, 0, 3], [700, 33, 1, 90, 400]
+    for shared in (None, 1):
+        c = Case(128, 8, 4, kvtc.FP32, 2, rows, lens, seed=31, shared=shared or 0)
+        c.fill()
+        q, out, lse, scale = run_attention(c, 4, shared=shared)
+        check_attention(c, q, out, lse, scale, True, "tight bounds")
+        wide = torch.full((5, 300), -1, dtype=torch.int32, device="cuda")
+        wide[:, :c.table_dev.shape[1]] = c.table_dev
+        c.table_dev = wide
+        for max_rows, max_len in ((8, 4800), (7, 700), (1000, 4800)):
+            c.batch = c.new_batch(rows, lens, max_rows=max_rows, max_len=max_len)
+            q2, out2, lse2, _ = run_attention(c, 4, shared=shared)
+            check_attention(c, q2, out2, lse2, scale, True, f"bounds {max_rows} {max_len}")
 
 
 def test_repeatable_and_on_other_streams():
