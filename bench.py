@@ -63,6 +63,12 @@ def parse():
     ap.add_argument("--pq-k2", type=int, default=64)
     ap.add_argument("--pq-outliers", type=int, default=64, help="outliers per (layer, head) and block")
     ap.add_argument("--pq-block", type=int, default=1024, help="tokens per outlier block")
+    ap.add_argument("--mx", action="store_true",
+                    help="time decode steps on the microscaled paged cache (append and attend) instead of the codec")
+    ap.add_argument("--mx-bits-k", type=int, default=4, choices=(4, 8))
+    ap.add_argument("--mx-bits-v", type=int, default=4, choices=(4, 8))
+    ap.add_argument("--mx-seqs", type=int, default=16, help="sequences of the batch")
+    ap.add_argument("--mx-group", type=int, default=4, help="query heads per KV head")
     ap.add_argument("--ceilings", action="store_true",
                     help="time plain read, write and copy kernels over 520 MB (the practical HBM ceilings) and exit")
     ap.add_argument("--copy-calibration", action="store_true",
@@ -658,6 +664,91 @@ def run_pq(args, w):
     print(json.dumps(res), flush=True)
 
 
+def run_mx(args, w):
+    """The microscaled paged cache in a serving loop: one step appends one
+    token per sequence and attends over every cached token, layer after
+    layer (kvtc_mx_write, kvtc_mx_attn), captured into one HIP graph.  The
+    metric is the cache bytes that the steps' attention reads per second."""
+    import torch
+
+    from tensor_compression_amd import kvtc, synth
+
+    K, V = synth.generate(w, device="cuda", tokens=args.tokens, layers=args.layers)
+    L, H, T, D = K.shape
+    n, G = args.mx_seqs, args.mx_group
+    end = T + args.warmup + args.steps + 1
+    pages = -(-end // 16)
+    dt = kvtc.BF16 if K.dtype == torch.bfloat16 else kvtc.FP32
+    cfg = dict(layers=L, kv_heads=H, head_dim=D, dtype=dt, bits_k=args.mx_bits_k, bits_v=args.mx_bits_v)
+    cache = kvtc.MxCache(cfg, n * pages)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    table = torch.randperm(n * pages, generator=g, device="cuda").to(torch.int32).view(n, pages)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), T, **i32)
+    for z in range(n):  # every sequence starts from the same cache, in pages of its own
+        one = cache.batch(table[z:z + 1], lens[:1], torch.tensor([0, T], **i32), total_rows=T, max_rows=T, max_len=end)
+        cache.write(one, K, V)
+    kd, vd = torch.empty_like(K), torch.empty_like(V)
+    cache.read(one, kd, vd)
+
+    batch = cache.batch(table, lens, torch.arange(n + 1, **i32), total_rows=n, max_rows=1, max_len=end)
+    qkv = torch.randn(n, (G + 2) * H, D, generator=g, device="cuda").to(K.dtype)
+    q, k, v = qkv.split([G * H, H, H], 1)
+    outs = [torch.empty(n, G * H, D, dtype=K.dtype, device="cuda") for _ in range(L)]
+    ws = cache.workspace(batch, G * H)
+    status = torch.zeros(1, **i32)
+
+    def step():
+        lens.add_(1)
+        for layer in range(L):
+            cache.write(batch, k, v, layer=layer, status=status)
+            cache.attention(batch, q, layer=layer, out=outs[layer], ws=ws, status=status)
+
+    step()
+    torch.cuda.synchronize()
+    lens.fill_(T)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(args.warmup):
+        graph.replay()
+    torch.cuda.synchronize()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    t0 = time.perf_counter()
+    e0.record()
+    for _ in range(args.steps):
+        graph.replay()
+    e1.record()
+    torch.cuda.synchronize()
+    wall = time.perf_counter() - t0
+    ms = e0.elapsed_time(e1) / args.steps
+    if int(status.item()) != 0:
+        raise SystemExit(f"device status {int(status.item())}")
+    token = cache.record_bytes // 16  # bytes of a token of one layer and head
+    mean_len = T + args.warmup + (args.steps + 1) / 2
+    read = n * mean_len * H * L * token
+    raw = 2 * D * K.element_size()
+
+    def nrmse(a, b):
+        a, b = a.float(), b.float()
+        return math.sqrt(float(((a - b) ** 2).sum()) / max(float((a ** 2).sum()), 1e-300))
+
+    print(json.dumps({
+        "metric": "microscaled cache GB/s read by decode steps", "value": read / (ms * 1e-3) / 1e9, "unit": "GB/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16" if dt == kvtc.BF16 else "fp32", "data": "synthetic",
+        "config": {"workload": f"{w.name}: {n} sequences of {T} tokens, {L} layers x {H} KV heads x head_dim {D}, "
+                               f"{G} query heads a KV head, keys {args.mx_bits_k} bits, values {args.mx_bits_v} bits",
+                   "layers": L, "kv_heads": H, "q_heads": G * H, "tokens": T, "head_dim": D, "seqs": n},
+        "wall_ms_per_step": wall * 1e3 / args.steps, "cache_bytes": cache.pool_bytes,
+        "compression_ratio": raw / token, "bits_per_value": 8.0 * token / (2 * D),
+        "nrmse_k": nrmse(K, kd), "nrmse_v": nrmse(V, vd),
+        "roofline": {"bound": "hbm", "kernels": ["k_mx_write", "k_mx_attn"], "algorithmic_bytes": read,
+                     "achieved": read / (ms * 1e-3) / 1e9, "peak": HBM_PEAK_GBPS, "unit": "GB/s",
+                     "frac": read / (ms * 1e-3) / 1e9 / HBM_PEAK_GBPS},
+    }), flush=True)
+
+
 def main():
     args = parse()
     if args.summarize_trace:
@@ -695,6 +786,9 @@ def main():
         return
     if args.pq:
         run_pq(args, w)
+        return
+    if args.mx:
+        run_mx(args, w)
         return
     if w.n_seqs > 0:
         run_paged(args, w)
