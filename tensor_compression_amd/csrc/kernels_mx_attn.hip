@@ -1,7 +1,7 @@
 // Attention over the microscaled paged cache.
 //
 // For 16 NT query rows of one kv head (row r = token r / G, head r % G of its
-// group) and a range of tokens, a workgroup of four waves computes
+// group) and a range of tokens, a workgroup computes
 //   s = q k^T, running maximum m, sum l of 2^(c s - m), o = sum 2^(c s - m) v
 // in one pass; its waves take pairs of pages in turn and are joined through
 // LDS at the end, ranges by k_mx_join.
@@ -373,13 +373,13 @@ __device__ __forceinline__ Work work_of(const MxAttnParams& p, int b) {
 // Few rows: memory bound, one pass over the codes with as many loads in
 // flight as the registers allow.  The waves take pairs of pages in turn, all
 // for the same 16 NT rows, and are joined at the end.
-template <int D>
+template <int D, int W>
 struct FewShared {
-  float o[4 * 16 * (D + 4)];
-  float2 ml[4][16];
+  float o[W * 16 * (D + 4)];
+  float2 ml[W][16];
 };
-template <int D, int BK, int BV, int NT, bool F32, bool ONCE>
-__device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewShared<D>& lds) {
+template <int D, int BK, int BV, int NT, bool F32, bool ONCE, int W>
+__device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewShared<D, W>& lds) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
   constexpr int C = D / 16;       // channels of an entry of the value groups
@@ -408,14 +408,14 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
   const int64_t page_bytes = (int64_t)p.H * R.bytes;
   const Sh sh(n, kg);
   const int p1 = (end + KVTC_MX_PAGE - 1) / KVTC_MX_PAGE;  // end of the range's pages
-  const int q0 = begin / KVTC_MX_PAGE + 2 * wave;          // this wave takes pages q0 + 8 k and q0 + 8 k + 1
-  const int steps = (p1 - q0 + 7) >> 3;
+  const int q0 = begin / KVTC_MX_PAGE + 2 * wave;          // this wave takes pages q0 + 2 W k and the one after
+  const int steps = (p1 - q0 + 2 * W - 1) / (2 * W);       // (not positive: none)
 
   // Page numbers: those of 32 steps at a time, one a lane, the next 32 steps'
   // on their way; -1 past the range and, once reported, outside the pool
   // (such pages are read as page 0 and masked).
   auto load_ids = [&](int step) {
-    const int pg = q0 + (step + (lane >> 1)) * 8 + (lane & 1);
+    const int pg = q0 + (step + (lane >> 1)) * 2 * W + (lane & 1);
     int id = -1;
     if (pg < p1) {
       id = table[pg];
@@ -477,7 +477,7 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
       ids = ids2;
       ids2 = load_ids(step + 32);
     }
-    const int t0 = (q0 + 8 * step) * KVTC_MX_PAGE;
+    const int t0 = (q0 + 2 * W * step) * KVTC_MX_PAGE;
     // tokens of page e that exist for this workgroup, 0 .. 16
     int have[2];
 #pragma unroll
@@ -581,16 +581,16 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
         *reinterpret_cast<float4*>(&lds.o[(wave * 16 + n) * OS + C * (4 * kg + i) + j]) = o;
       }
     if (kg == 0) lds.ml[wave][n] = make_float2(sm.m[t], sum);
-    const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * C;
+    const int r = (threadIdx.x >> 4) & 15, c0 = (threadIdx.x & 15) * C;
     const int row = __shfl(rw.at[t], r), hq = __shfl(rw.head[t], r);
     __syncthreads();
-    if (row < 0) continue;
+    if (row < 0 || wave >= 4) continue;
     const int64_t at = (int64_t)row * Hq + hq;
-    float M = kLow, L = 0.f, a[4];
+    float M = kLow, L = 0.f, a[W];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = fmaxf(M, lds.ml[w][r].x);
+    for (int w = 0; w < W; ++w) M = fmaxf(M, lds.ml[w][r].x);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < W; ++w) {
       a[w] = __builtin_amdgcn_exp2f(lds.ml[w][r].x - M);
       L = __fmaf_rn(a[w], lds.ml[w][r].y, L);
     }
@@ -599,7 +599,7 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
     for (int j = 0; j < C; j += 4) {
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float4 x = *reinterpret_cast<const float4*>(&lds.o[(w * 16 + r) * OS + c0 + j]);
         s.x = __fmaf_rn(a[w], x.x, s.x);
         s.y = __fmaf_rn(a[w], x.y, s.y);
@@ -620,10 +620,10 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
   }
 }
 
-template <int D, int BK, int BV, int NT, bool F32, bool ONCE>
-__global__ __launch_bounds__(256, NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const MxAttnParams p) {
-  __shared__ __attribute__((aligned(16))) FewShared<D> lds;
-  few_rows<D, BK, BV, NT, F32, ONCE>(p, blockIdx.x, lds);
+template <int D, int BK, int BV, int NT, bool F32, bool ONCE, int W>
+__global__ __launch_bounds__(W * 64, W == 4 && NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const MxAttnParams p) {
+  __shared__ __attribute__((aligned(16))) FewShared<D, W> lds;
+  few_rows<D, BK, BV, NT, F32, ONCE, W>(p, blockIdx.x, lds);
 }
 
 // Many rows: bound by the issue of matrix and vector instructions.  A
@@ -938,10 +938,10 @@ template <int D, int BK, int BV, bool F32>
 __global__ __launch_bounds__(256, 2) void k_mx_both(const MxAttnParams prefix, const MxAttnParams own, int prefix_blocks) {
   __shared__ __attribute__((aligned(16))) union {
     ManyShared<D> many;
-    FewShared<D> few;
+    FewShared<D, 4> few;
   } lds;
   if ((int)blockIdx.x < prefix_blocks) many_rows<D, BK, BV, F32>(prefix, blockIdx.x, lds.many);
-  else few_rows<D, BK, BV, 1, F32, false>(own, (int)blockIdx.x - prefix_blocks, lds.few);
+  else few_rows<D, BK, BV, 1, F32, false, 4>(own, (int)blockIdx.x - prefix_blocks, lds.few);
 }
 
 // Joins a row's partials: W waves a (row, head), sixteen lanes on its
@@ -1025,14 +1025,17 @@ template <int D, int BK, int BV, bool F32>
 void launch_pass(const MxAttnParams& p, hipStream_t s) {
   const unsigned grid = blocks_of(p);
   if (p.nt == 1) {
-    if (p.once) k_mx_attn<D, BK, BV, 1, F32, true><<<grid, 256, 0, s>>>(p);
-    else k_mx_attn<D, BK, BV, 1, F32, false><<<grid, 256, 0, s>>>(p);
-  } else if (p.nt == 2) k_mx_attn<D, BK, BV, 2, F32, false><<<grid, 256, 0, s>>>(p);
+    if (p.waves == 8) {
+      if (p.once) k_mx_attn<D, BK, BV, 1, F32, true, 8><<<grid, 512, 0, s>>>(p);
+      else k_mx_attn<D, BK, BV, 1, F32, false, 8><<<grid, 512, 0, s>>>(p);
+    } else if (p.once) k_mx_attn<D, BK, BV, 1, F32, true, 4><<<grid, 256, 0, s>>>(p);
+    else k_mx_attn<D, BK, BV, 1, F32, false, 4><<<grid, 256, 0, s>>>(p);
+  } else if (p.nt == 2) k_mx_attn<D, BK, BV, 2, F32, false, 4><<<grid, 256, 0, s>>>(p);
   else k_mx_rows<D, BK, BV, F32><<<grid, 256, 0, s>>>(p);
 }
 template <int D, int BK, int BV, bool F32>
 hipError_t launch_format(const MxAttnParams* prefix, const MxAttnParams* own, hipStream_t s) {
-  if (prefix && own && prefix->nt == 8 && own->nt == 1 && !own->once) {
+  if (prefix && own && prefix->nt == 8 && own->nt == 1 && own->waves == 4 && !own->once) {
     const unsigned n = blocks_of(*prefix);
     k_mx_both<D, BK, BV, F32><<<n + blocks_of(*own), 256, 0, s>>>(*prefix, *own, (int)n);
     return hipGetLastError();

@@ -117,6 +117,7 @@ kvtc_status io_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t l
 // How one pass of the attention is cut up.
 struct Cut {
   int nt;             // 16-row tiles of a workgroup: 1 or 2 (k_mx_attn), 8 (k_mx_rows)
+  int waves;          // waves of a workgroup
   int64_t tiles;      // workgroups along the rows
   int nsplit, chunk;  // workgroups along the tokens, tokens of each
 };
@@ -129,13 +130,18 @@ Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span) {
   // partials to join), two for many rows, which need the second's waves (128
   // sequences behind 32768 tokens: 220 us with 256, 166 with 512) unless
   // that left them less than 512 tokens each (64 behind 8192: 41 and 52 us).
-  // Sequences of few rows stay whole up to 640 tokens: a step of 128 tokens
-  // costs 0.55 us, a second launch and its join 2.8 us.
   const int64_t units = c.tiles * H * seqs, room = c.nt == 8 ? 512 : 256;
-  const int64_t most = c.nt == 8 ? span / 512 : span <= 640 ? 1 : (span + 127) / 128;
-  const int64_t n = std::max<int64_t>(1, std::min(room / units, most));
+  int64_t n = std::max<int64_t>(1, std::min(room / units, c.nt == 8 ? span / 512 : (span + 127) / 128));
+  // A second launch and its join cost about 3 us, what a workgroup takes for
+  // 800 tokens (16 sequences of 1000 tokens: whole 8.2, halved 9.7 us; 1
+  // sequence of 1000: whole 7.9, in eight 7.3 us).
+  if (c.nt != 8 && span - span / n <= 800) n = 1;
   c.chunk = (int)(((span + n - 1) / n + 127) / 128 * 128);
   c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / std::max(c.chunk, 1));
+  // Eight waves where a CU has one workgroup with enough for all of them (24
+  // sequences of 16000 tokens: 114 -> 79 us); beside others, or with little
+  // to do, four (40 of 4000: 34 us, eight 40; 1 of 8000 in 256s: 8.7 and 9.0).
+  c.waves = c.nt == 1 && units <= 256 && c.chunk > 512 ? 8 : 4;
   return c;
 }
 
@@ -155,7 +161,10 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   a->begin = (int)std::min<int64_t>((int64_t)shared * KVTC_MX_PAGE, b.max_len);
   const int64_t rows = (int64_t)std::min(b.max_rows, b.total_rows) * G;
   if (a->begin < b.max_len || a->begin == 0) a->own = cut_pass(rows, b.n_seqs, c.kv_heads, b.max_len - a->begin);
-  if (a->begin > 0) a->prefix = cut_pass((int64_t)b.total_rows * G, 1, c.kv_heads, a->begin);
+  if (a->begin > 0) {
+    a->own.waves = 4;  // beside the prefix's workgroups
+    a->prefix = cut_pass((int64_t)b.total_rows * G, 1, c.kv_heads, a->begin);
+  }
   a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
   if (a->own.tiles * c.kv_heads * std::max(a->own.nsplit, 1) * b.n_seqs > kMaxGrid ||
@@ -202,6 +211,7 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   }
   auto cut = [&](const Cut& c) {
     p.nt = c.nt;
+    p.waves = c.waves;
     p.tiles = (int32_t)c.tiles;
     p.nsplit = c.nsplit;
     p.chunk = c.chunk;
