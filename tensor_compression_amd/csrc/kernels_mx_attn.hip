@@ -373,19 +373,25 @@ __device__ __forceinline__ Work work_of(const MxAttnParams& p, int b) {
 // Few rows: memory bound, one pass over the codes with as many loads in
 // flight as the registers allow.  The waves take pairs of pages in turn, all
 // for the same 16 NT rows, and are joined at the end.
-template <int D, int W>
+// The smallest parts of 32 fp32 queries of 128 channels stay in LDS, for the
+// registers (64 sequences of 3 rows and 3000 tokens, k8v8: 119 -> 99 us).
+template <int D, int NT, bool F32>
+constexpr bool few_tight = F32 && D == 128 && NT == 2;
+template <int D, int NT, bool F32, int W>
 struct FewShared {
+  uint4 q[few_tight<D, NT, F32> ? NT : 0][D / 32][64];  // row tile, contraction step, lane
   float o[W * 16 * (D + 4)];
   float2 ml[W][16];
 };
 template <int D, int BK, int BV, int NT, bool F32, bool ONCE, int W>
-__device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewShared<D, W>& lds) {
+__device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewShared<D, NT, F32, W>& lds) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
   constexpr int C = D / 16;       // channels of an entry of the value groups
   constexpr int KS = D / 32;      // contraction steps of S
   constexpr int NP = F32 ? 3 : 1;  // bf16 parts of queries and weights
   constexpr int OS = D + 4;       // row stride of the joining buffer
+  constexpr bool TIGHT = few_tight<D, NT, F32>;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, kg = lane >> 4;
@@ -458,6 +464,14 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
 #pragma unroll
     for (int s = 0; s < KS; ++s)
       load_query<F32>(p, rw.at[t] * p.q_stride + rw.head[t] * D + (D / 4) * kg + 8 * s, rw.at[t] >= 0, qf[t][s]);
+  if constexpr (TIGHT) {  // (all waves have the same rows)
+    if (wave == 0)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) lds.q[t][s][lane] = __builtin_bit_cast(uint4, qf[t][s][2]);
+    __syncthreads();
+  }
   if (steps > 0) {
     load_keys(0, false);
     load_values();
@@ -509,6 +523,8 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
     }
 
     f32x4_t sa[NT][2];
+    int ql = lane;
+    if constexpr (TIGHT) asm volatile("" : "+v"(ql));  // read in every step, not kept from the first
     {
       bf16x8_t kf[2][KS];
 #pragma unroll
@@ -526,7 +542,12 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
 #pragma unroll
           for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sa[t][e] = mfma(kf[e][s], qf[t][s][kp], sa[t][e]);
+            for (int e = 0; e < 2; ++e) {
+              bf16x8_t q = qf[t][s][kp];
+              if constexpr (TIGHT)
+                if (kp == 2) q = __builtin_bit_cast(bf16x8_t, lds.q[t][s][ql]);
+              sa[t][e] = mfma(kf[e][s], q, sa[t][e]);
+            }
       }
     }
     if (!whole) {
@@ -622,7 +643,7 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
 
 template <int D, int BK, int BV, int NT, bool F32, bool ONCE, int W>
 __global__ __launch_bounds__(W * 64, W == 4 && NT == 1 && !F32 ? 3 : 2) void k_mx_attn(const MxAttnParams p) {
-  __shared__ __attribute__((aligned(16))) FewShared<D, W> lds;
+  __shared__ __attribute__((aligned(16))) FewShared<D, NT, F32, W> lds;
   few_rows<D, BK, BV, NT, F32, ONCE, W>(p, blockIdx.x, lds);
 }
 
@@ -640,8 +661,16 @@ __global__ __launch_bounds__(W * 64, W == 4 && NT == 1 && !F32 ? 3 : 2) void k_m
 // the slice of P^T that the product with 16 tokens' values takes from it.
 // Value rows of a 32-channel product: row n + 16 o is channel 2 ct + o of
 // entry n of the value groups.
-template <int D>
+// fp32 queries of 128 channels do not fit the registers next to the rest: the
+// smallest parts of all but 16 channels go to LDS, as many as leave room for
+// two workgroups a CU, and one tile's codes are on their way instead of three
+// (2048 rows on 4096 tokens: k4v4 545 -> 490 us, k8v8 706 -> 455; 64 channels
+// fit: 241 us, 250 this way).
+template <int D, bool F32>
+constexpr bool many_tight = F32 && D == 128;
+template <int D, bool F32>
 struct ManyShared {
+  uint4 q[4][many_tight<D, F32> ? D / 16 - 1 : 0][64];  // wave, contraction step, lane
   struct Tile {
     uint4 k[D / 16][64];     // contraction step, operand lane
     uint4 v[2][D / 32][64];  // page, channel tile, operand lane
@@ -651,14 +680,16 @@ struct ManyShared {
   int odd[4];  // per wave: it met a page outside the pool, so every tile's state is looked at
 };
 template <int D, int BK, int BV, bool F32>
-__device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, ManyShared<D>& lds) {
+__device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, ManyShared<D, F32>& lds) {
   using Sh = Share<D, BK, BV>;
   constexpr MxRecord R = Sh::R;
   constexpr int C = D / 16, KS = D / 32, QS = D / 16, CT = D / 32, NP = F32 ? 3 : 1;
+  constexpr bool TIGHT = many_tight<D, F32>;
+  constexpr int NR = TIGHT ? 1 : 3;  // codes of so many tiles in registers
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, kg = lane >> 4, hh = lane >> 5;
-  using Tile = typename ManyShared<D>::Tile;
+  using Tile = typename ManyShared<D, F32>::Tile;
   Tile(&tile)[3] = lds.tile;
   const Work wk = work_of(p, block);
   const int h = wk.h;
@@ -721,11 +752,13 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
     g.ks = rec[sh.ks];
     g.vs = *reinterpret_cast<const uint32_t*>(rec + sh.vs);
   };
-  // Codes of tile t in raw[t % 3]: those of tile t + 2 are converted while
-  // those of t + 3 and t + 4 are on their way (2000 clocks from the request on).
-  Raw raw[3];
+  // Codes of tile t in raw[t % NR]: those of tile t + 2 are converted while
+  // those of t + 3 and t + 4 are on their way (2000 clocks from the request
+  // on); TIGHT: then those of t + 3 are requested, a step ahead, which takes
+  // as long with three times the products.
+  Raw raw[NR];
 #pragma unroll
-  for (int t = 0; t < 3; ++t) load_page(raw[t], id_of(t));
+  for (int t = 0; t < NR; ++t) load_page(raw[t], id_of(t));
 
   Rows<1> rw = rows_of<1>(p, sq, h, wk.tile * 128 + wave * 32, rows, lane & 31);
   {  // rows_of looks at the first 16 lanes
@@ -738,6 +771,9 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
 #pragma unroll
   for (int c = 0; c < QS; ++c)
     load_query<F32>(p, rw.at[0] * p.q_stride + rw.head[0] * D + 16 * c + 8 * hh, rw.at[0] >= 0, qf[c]);
+  if constexpr (TIGHT)  // (only this wave reads them)
+#pragma unroll
+    for (int c = 0; c < QS - 1; ++c) lds.q[wave][c][lane] = __builtin_bit_cast(uint4, qf[c][2]);
   if (lane == 0) lds.bounds[wave] = make_int2(rw.lo, rw.hi);
   __syncthreads();
   int lo = 0x7FFFFFFF, hi = 0;  // of all four waves
@@ -810,16 +846,22 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
 #pragma unroll
     for (int kp = NP - 1; kp >= 0; --kp)  // small parts first
 #pragma unroll
-      for (int c = 0; c < QS; ++c) s = mfma(__builtin_bit_cast(bf16x8_t, from.k[c][lane]), qf[c][kp], s);
+      for (int c = 0; c < QS; ++c) {
+        bf16x8_t q = qf[c][kp];
+        if constexpr (TIGHT)
+          if (kp == 2 && c < QS - 1) q = __builtin_bit_cast(bf16x8_t, lds.q[wave][c][lane]);
+        s = mfma(__builtin_bit_cast(bf16x8_t, from.k[c][lane]), q, s);
+      }
   };
 
   if (tiles > 0) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      clean(raw[t], t, tile[t]);
-      convert(raw[t], tile[t]);
+      clean(raw[t % NR], t, tile[t]);
+      convert(raw[t % NR], tile[t]);
+      if (TIGHT) load_page(raw[0], id_of(t + 1));
     }
-    load_page(raw[0], id_of(3));
+    if (!TIGHT) load_page(raw[0], id_of(3));
     __syncthreads();
     scores(tile[0], sa);
   }
@@ -827,7 +869,7 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
   auto step = [&](int t, auto bc) {
     constexpr int b = decltype(bc)::value;  // t % 3
     Tile &now = tile[b], &next = tile[(b + 1) % 3], &after = tile[(b + 2) % 3];
-    Raw &use = raw[(b + 2) % 3], &load = raw[(b + 1) % 3];
+    Raw &use = raw[(b + 2) % NR], &load = raw[(b + 1) % NR];
     const int t0 = (p0 + 2 * t) * KVTC_MX_PAGE;
     // the page numbers of tile t were read at least 64 tiles, or the opening barrier, ago
     if ((t & 63) == 0) slow = __builtin_amdgcn_readfirstlane(lds.odd[0] | lds.odd[1] | lds.odd[2] | lds.odd[3]);
@@ -863,10 +905,10 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
         for (int c = 0; c < CT; ++c) acc[c] *= a;
       }
     }
-    clean(use, t + 2, after);
-    const int id = id_of(t + 4);
+    if (!TIGHT) clean(use, t + 2, after);
+    const int id = id_of(TIGHT ? t + 3 : t + 4);
     __syncthreads();  // tile t + 1 is in its buffer, nobody reads tile t - 1 any more
-    load_page(load, id);
+    if (!TIGHT) load_page(load, id);
     __builtin_amdgcn_sched_barrier(0);  // the loads first
     __builtin_amdgcn_s_setprio(1);
     float w[16];
@@ -893,7 +935,9 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
 #pragma unroll
         for (int kp = NP - 1; kp >= 0; --kp) acc[c] = mfma(vf, pf[u][kp], acc[c]);
       }
+    if (TIGHT) clean(use, t + 2, after);
     convert(use, after);
+    if (TIGHT) load_page(use, id);
     __builtin_amdgcn_s_setprio(0);
   };
   for (int t = 0; t < tiles; t += 3) {
@@ -927,7 +971,7 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
 
 template <int D, int BK, int BV, bool F32>
 __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
-  __shared__ __attribute__((aligned(16))) ManyShared<D> lds;
+  __shared__ __attribute__((aligned(16))) ManyShared<D, F32> lds;
   many_rows<D, BK, BV, F32>(p, blockIdx.x, lds);
 }
 
@@ -937,8 +981,8 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
 template <int D, int BK, int BV, bool F32>
 __global__ __launch_bounds__(256, 2) void k_mx_both(const MxAttnParams prefix, const MxAttnParams own, int prefix_blocks) {
   __shared__ __attribute__((aligned(16))) union {
-    ManyShared<D> many;
-    FewShared<D, 4> few;
+    ManyShared<D, F32> many;
+    FewShared<D, 1, F32, 4> few;
   } lds;
   if ((int)blockIdx.x < prefix_blocks) many_rows<D, BK, BV, F32>(prefix, blockIdx.x, lds.many);
   else few_rows<D, BK, BV, 1, F32, false, 4>(own, (int)blockIdx.x - prefix_blocks, lds.few);
