@@ -637,8 +637,8 @@ kvtc_status kvtc_mx_attn_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batc
  * kv head h / (q_heads / kv_heads)), row r of head h at r q_stride +
  * h head_dim.  out: device [total_rows, q_heads, head_dim] in cfg->dtype;
  * lse: device fp32 [total_rows, q_heads] or NULL.  A row that attends to
- * nothing gets zeros and lse -infinity.  scale must be positive, finite and
- * a normal number.
+ * nothing gets zeros and lse -infinity.  scale must be a positive normal
+ * number, at most 2^100.
  * A NaN token affects the rows that attend to it and no others.
  *
  * Products are exact (bf16 queries) and summed in fp32, the softmax is fp32;

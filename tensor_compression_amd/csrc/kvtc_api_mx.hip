@@ -185,7 +185,7 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   st = plan_attn(*cfg, *b, q_heads, shared, &a);
   if (st != KVTC_OK) return st;
   const int elem = cfg->dtype == KVTC_BF16 ? 2 : 4;
-  if (!(scale > 0.0f) || !isnormal(scale) || (causal != 0 && causal != 1)) return KVTC_ERR_INVALID_ARG;
+  if (!(scale > 0.0f && scale <= 0x1p100f) || !isnormal(scale) || (causal != 0 && causal != 1)) return KVTC_ERR_INVALID_ARG;
   if (q_stride < 0 || q_stride > ((int64_t)1 << 46) || (q_stride * elem) % 16) return KVTC_ERR_INVALID_ARG;
   if (nothing_to_do(*b)) return KVTC_OK;
   if (!q || !out || misaligned(q) || misaligned(out) || misaligned(lse, 4) || misaligned(ws)) return KVTC_ERR_INVALID_ARG;

@@ -566,6 +566,8 @@ class MxBatch:
         for t, shape in ((page_table, (n, page_table.shape[-1])), (kv_lens, (n,)), (row_start, (n + 1,))):
             if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError("page_table [n, pages], kv_lens [n] and row_start [n + 1] are contiguous int32")
+        if max(total_rows, max_rows, max_len) >= 2 ** 31:
+            raise ValueError("bounds are 32-bit")
         self.page_table, self.kv_lens, self.row_start = page_table, kv_lens, row_start
         self.index = page_table.get_device()
         self.total_rows, self.max_rows, self.max_len = total_rows, max_rows, max_len
@@ -650,12 +652,11 @@ class MxCache:
             arr = self._strides[key] = (ctypes.c_int64 * 3)(*key)
         return x.data_ptr(), arr
 
-    @staticmethod
-    def _status(status):
+    def _status(self, status):
         if status is None:
             return None
-        if status.dtype != torch.int32 or status.numel() < 1 or not status.is_cuda:
-            raise ValueError("status is an int32 tensor on the device")
+        if status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != self._index:
+            raise ValueError("status is an int32 tensor on the cache's device")
         return status.data_ptr()
 
     def write(self, batch: MxBatch, k: torch.Tensor, v: torch.Tensor, layer: int = 0,

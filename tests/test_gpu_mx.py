@@ -340,6 +340,30 @@ def test_attention_long_ranges(dtype):
     assert c.status.item() == 0
 
 
+@pytest.mark.parametrize("D,bk,bv,dtype", [(128, 4, 4, kvtc.BF16), (128, 8, 4, kvtc.FP32), (64, 4, 8, kvtc.BF16),
+                                           (64, 8, 8, kvtc.FP32)])
+def test_attention_one_workgroup_a_unit(D, bk, bv, dtype):
+    """About as many sequences and heads as compute units, each long enough for
+    a larger workgroup; under bounds of hundreds of megabytes of codes too."""
+    n, H = 30, 8
+    lens = [1500 - 29 * z for z in range(n - 6)] + [0, 1, 16, 17, 255, 257]
+    c = Case(D, bk, bv, dtype, H, [1], [1500], seed=D + bk)
+    c.fill()
+    q = c.rand(n + 1, 2 * H, D)
+    table = torch.full((n, 640), 2 ** 30, dtype=torch.int32, device="cuda")
+    table[:, :94] = c.table_dev[:1, :94]
+    kv, starts = dev(lens, torch.int32), dev(list(range(n + 1)), torch.int32)
+    for max_len in (1500, 10240):
+        b = c.cache.batch(table, kv, starts, total_rows=n + 1, max_rows=1, max_len=max_len)
+        lse = torch.full((n + 1, 2 * H), 7.0, device="cuda")
+        out = torch.full_like(q, 7.0)
+        c.cache.attention(b, q, out=out, lse=lse, status=c.status)
+        assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all() and c.status.item() == 0
+        for z in (0, 11, 24, 25, 26, 27, 28, 29):
+            c.lens = [lens[z]]
+            check_attention(c, q[z:z + 1], out[z:z + 1], lse[z:z + 1], D ** -0.5, True, f"sequence {z} bound {max_len}")
+
+
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 8.0])
 def test_attention_scales(scale):
     """Flat and needle-sharp weights, scores that grow along the sequence."""

@@ -174,7 +174,8 @@ def test_overlapping_outputs():
 def test_bad_attention(name):
     for bad in (dict(q=None), dict(out=None), dict(q=P + 2), dict(out=P + 8), dict(lse=P + 2), dict(ws=P + 8),
                 dict(q_stride=-8), dict(q_stride=12), dict(q_heads=0), dict(q_heads=6), dict(q_heads=2),
-                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(causal=2)):
+                dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=2.0 ** 101),
+                dict(scale=2.0 ** -127), dict(causal=2)):
         assert call(name, **bad) == INV, bad
     big = batch(total_rows=2 ** 28)
     assert call(name, b=big, q_heads=8) == UNS
