@@ -139,7 +139,7 @@ def traffic_from_profile(phase, path=TRAFFIC_FILE):
 
 
 def _short_kernel(name: str) -> str:
-    n = name.split("(")[0].replace("void ", "")
+    n = name.replace("(anonymous namespace)::", "").split("(")[0].replace("void ", "")
     return n.replace("kvtc::", "")
 
 

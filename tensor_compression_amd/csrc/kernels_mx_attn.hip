@@ -3,8 +3,9 @@
 // For 16 NT query rows of one kv head (row r = token r / G, head r % G of its
 // group) and a range of tokens, a workgroup computes
 //   s = q k^T, running maximum m, sum l of 2^(c s - m), o = sum 2^(c s - m) v
-// in one pass; its waves take pairs of pages in turn and are joined through
-// LDS at the end, ranges by k_mx_join.
+// in one pass.  Up to 64 rows its waves take pairs of pages in turn and are
+// joined through LDS at the end (k_mx_attn); more rows share the converted
+// codes in LDS (k_mx_rows); ranges of tokens are joined by k_mx_join.
 //
 // The pool is laid out for v_mfma_f32_16x16x32_bf16, so nothing is shuffled
 // or staged on its way to the matrix unit:
@@ -174,6 +175,9 @@ __device__ __forceinline__ Rows<NT> rows_of(const MxAttnParams& p, const MxSeq& 
 }
 
 // Eight fp32 values as one bf16 operand, or as three whose sum keeps 24 bits.
+// One for bf16 outputs: rounding a weight costs half a step of 2^-8 of it, and
+// an average of values off by at most that is what the output is rounded to
+// anyway; the sum l is of the unrounded weights, in fp32.  Three for fp32.
 template <int NP>
 __device__ __forceinline__ void split8(float (&x)[8], bf16x8_t (&o)[NP]) {
 #pragma unroll
@@ -370,9 +374,14 @@ __device__ __forceinline__ Work work_of(const MxAttnParams& p, int b) {
   return w;
 }
 
-// Few rows: memory bound, one pass over the codes with as many loads in
-// flight as the registers allow.  The waves take pairs of pages in turn, all
-// for the same 16 NT rows, and are joined at the end.
+// Few rows: one pass over the codes with as many loads in flight as the
+// registers allow.  The W waves take pairs of pages in turn, all for the same
+// 16 NT rows, and are joined at the end.  Bound by memory where the card is
+// full (64 sequences of 4300 tokens and 8 heads, 4 bits: 309 MB in 67 us, 4.6
+// TB/s; one of 131072, keys in 8 bits: 210 MB in 40 us, 5.2 TB/s), by vector
+// issue (173 instructions a wave and 32 tokens, about 45 GB/s a CU) where a
+// unit has one workgroup, and by the launch and four loads in a row (row
+// bounds, page numbers, codes, values) at a few hundred tokens (500: 6.5 us).
 // The smallest parts of 32 fp32 queries of 128 channels stay in LDS, for the
 // registers (64 sequences of 3 rows and 3000 tokens, k8v8: 119 -> 99 us).
 template <int D, int NT, bool F32>
@@ -647,8 +656,10 @@ __global__ __launch_bounds__(W * 64, W == 4 && NT == 1 && !F32 ? 3 : 2) void k_m
   few_rows<D, BK, BV, NT, F32, ONCE, W>(p, blockIdx.x, lds);
 }
 
-// Many rows: bound by the issue of matrix and vector instructions.  A
-// workgroup takes 128 rows, 32 a wave, and walks over the tokens 32 at a
+// Many rows: bound by the issue of matrix and vector instructions (2048 rows
+// of 4 heads on 4096 tokens before them: 173 GFLOP in 174 to 196 us, as the
+// clock allows; the matrix unit is busy for 42% of the clocks, vector
+// instructions issue in 51%, two waves a SIMD).  A workgroup takes 128 rows, 32 a wave, and walks over the tokens 32 at a
 // time; each wave turns half of a page into operands in LDS, in the order in
 // which all four read them back, so a code is converted once for 128 rows.
 // Three buffers, so that in one stretch between barriers a wave multiplies
