@@ -129,7 +129,8 @@ Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span) {
   // (1 sequence of 131072 tokens: 41 us with 256, 42 with 768, and more
   // partials to join), two for many rows, which need the second's waves (128
   // sequences behind 32768 tokens: 220 us with 256, 166 with 512) unless
-  // that left them less than 512 tokens each (64 behind 8192: 41 and 52 us).
+  // that left them less than 512 tokens each (64 behind 8192: 25 us and 6 for
+  // the join, with ranges of 256 29 and 8).
   const int64_t units = c.tiles * H * seqs, room = c.nt == 8 ? 512 : 256;
   int64_t n = std::max<int64_t>(1, std::min(room / units, c.nt == 8 ? span / 512 : (span + 127) / 128));
   // A second launch and its join cost about 3 us, what a workgroup takes for
