@@ -546,6 +546,36 @@ def test_loose_bounds_give_the_same():
             check_attention(c, q2, out2, lse2, scale, True, f"bounds {max_rows} {max_len}")
 
 
+def test_pool_offsets_past_32_bits():
+    """The same tokens in a small pool and in the last pages of one of 4.5 GB,
+    behind a whole layer: the same bytes, values and outputs."""
+    H, D, ln = 8, 128, 700
+    pages, last = -(-ln // 16), 65000
+    cfg = dict(layers=2, kv_heads=H, head_dim=D, dtype=kvtc.BF16, bits_k=8, bits_v=8)
+    c = Case(D, 8, 8, kvtc.BF16, H, [1], [ln], seed=16)
+    k, v = c.rand(ln, H, D), c.rand(ln, H, D)
+    got = []
+    for n in (pages, last):
+        cache = kvtc.MxCache(cfg, n)
+        table = dev([list(range(n - 1, n - 1 - pages, -1))], torch.int32)
+
+        def batch(rows):
+            return cache.batch(table, dev([ln], torch.int32), dev([0, rows], torch.int32), rows, rows, ln)
+
+        cache.write(batch(ln), k, v, layer=1, status=c.status)
+        ko, vo = torch.empty_like(k), torch.empty_like(v)
+        cache.read(batch(ln), ko, vo, layer=1, status=c.status)
+        outs = [cache.pool[1, table[0].long()], ko, vo]
+        for rows in (2, 17, 200):
+            q = k[:rows].repeat(1, 2, 1) + v[:rows].repeat(1, 2, 1)
+            outs.append(cache.attention(batch(rows), q, layer=1, status=c.status))
+            outs.append(cache.attention_shared(batch(rows), q, 20, layer=1, status=c.status))
+        got.append(outs)
+    assert last * H * cache.record_bytes * 2 > 2 ** 32 and c.status.item() == 0
+    for small, big in zip(*got):
+        assert torch.equal(small, big) and not torch.isnan(big.float()).any()
+
+
 def test_repeatable_and_on_other_streams():
     c = Case(128, 4, 8, kvtc.BF16, 2, [1] * 6, [900, 3, 77, 2000, 512, 1], seed=13)
     c.fill()
