@@ -374,11 +374,45 @@ __device__ __forceinline__ Work work_of(const MxAttnParams& p, int b) {
   return w;
 }
 
+// The sequence that is number `rank` (below n_seqs, at most 256 of them) when
+// they are taken from the longest on, to 1/256 of max_len, equal ones in their
+// order.  Every wave finds it for itself.
+__device__ __forceinline__ int by_length(const kvtc_mx_batch& b, int rank) {
+  const int lane = threadIdx.x & 63, shift = max(24 - __builtin_clz(b.max_len | 1), 0);
+  int key[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int i = 64 * w + lane;
+    key[w] = i < b.n_seqs ? min(max(b.kv_lens[i], 0), b.max_len) >> shift : -1;
+  }
+  auto at_least = [&](int v) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (64 * w < b.n_seqs) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[w] >= v));
+    return n;
+  };
+  int v = 0;
+#pragma unroll
+  for (int bit = 128; bit; bit >>= 1)
+    if (at_least(v + bit) > rank) v += bit;
+  int left = rank - at_least(v + 1), z = 0;  // those of length v that come before it
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint64_t same = __builtin_amdgcn_ballot_w64(key[w] == v);
+    const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+    const uint64_t it = __builtin_amdgcn_ballot_w64(key[w] == v && before == left);
+    if (it) z = 64 * w + __builtin_ctzll(it);
+    left -= __builtin_popcountll(same);
+  }
+  return z;
+}
+
 // Few rows: one pass over the codes with as many loads in flight as the
 // registers allow.  The W waves take pairs of pages in turn, all for the same
 // 16 NT rows, and are joined at the end.  Bound by memory where the card is
-// full (64 sequences of 4300 tokens and 8 heads, 4 bits: 309 MB in 67 us, 4.6
-// TB/s; one of 131072, keys in 8 bits: 210 MB in 40 us, 5.2 TB/s), by vector
+// full (64 sequences of 511 to 8191 tokens and 8 heads, 4 bits: 309 MB in 62 us,
+// 5.0 TB/s; one of 131072, keys in 8 bits: 210 MB in 40 us, 5.2 TB/s), by vector
 // issue (173 instructions a wave and 32 tokens, about 45 GB/s a CU) where a
 // unit has one workgroup, and by the launch and four loads in a row (row
 // bounds, page numbers, codes, values) at a few hundred tokens (500: 6.5 us).
@@ -404,8 +438,10 @@ __device__ __forceinline__ void few_rows(const MxAttnParams& p, int block, FewSh
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int n = lane & 15, kg = lane >> 4;
-  const Work wk = work_of(p, block);
+  Work wk = work_of(p, block);
   const int h = wk.h;
+  if constexpr (W == 4)
+    if (p.pair) wk.z = by_length(p.b, wk.z < p.pair ? p.pair - 1 - wk.z : wk.z);
 
   const int Hq = p.H * p.G;
   MxSeq sq{0, 0, 0};

@@ -227,6 +227,15 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   p.end = 0x7FFFFFFF;
   p.slot0 = a.prefix.nsplit;
   p.fold = causal && a.own.nt == 8 && a.own.tiles * cfg->kv_heads * a.own.nsplit * b->n_seqs <= 512;
+  // Whole sequences, more workgroups than compute units: first the longest, one
+  // a unit and in rising order, then the others from the longest on, so that
+  // the second of a unit makes up for its first (sequences of 511 to 8191 tokens, 8 heads: 64 of
+  // them 67 -> 62 us, 128 115 -> 94; all of 4000: 64 46.7 -> 47.7, so not where
+  // they are short).
+  const int64_t per_round = std::max(256 / cfg->kv_heads, 1);
+  if (!a.prefix.nsplit && a.own.nt < 8 && a.own.tiles == 1 && a.own.nsplit == 1 && b->n_seqs > per_round &&
+      b->n_seqs <= 256 && b->max_len >= 2048)
+    p.pair = (int32_t)per_round;
   // at most this many bytes of codes, against the 256 MB of the memory-side cache
   p.once = (int64_t)b->n_seqs * (b->max_len - a.begin) / KVTC_MX_PAGE * cfg->kv_heads *
                mx_record(cfg->head_dim, cfg->bits_k, cfg->bits_v).bytes > ((int64_t)256 << 20);

@@ -364,6 +364,36 @@ def test_attention_one_workgroup_a_unit(D, bk, bv, dtype):
             check_attention(c, q[z:z + 1], out[z:z + 1], lse[z:z + 1], D ** -0.5, True, f"sequence {z} bound {max_len}")
 
 
+@pytest.mark.parametrize("n,H,G", [(33, 8, 1), (64, 8, 5), (65, 5, 1), (150, 2, 1), (256, 2, 1), (257, 1, 1), (300, 1, 20)])
+def test_attention_sequences_by_length(n, H, G):
+    """More whole sequences than compute units take: every length, equal ones,
+    0 and the longest, each computed once; lengths outside the bounds too."""
+    D, longest = 64, 2100
+    c = Case(D, 4, 8, kvtc.BF16, H, [1], [longest], seed=n)
+    c.fill()
+    lens = [int(x) for x in c.rng.integers(0, longest + 1, n)]
+    lens[3], lens[7], lens[8], lens[9], lens[n - 1] = longest, 0, 900, 900, 901
+    q = c.rand(n, H * G, D)
+    table = c.table_dev.expand(n, -1).contiguous()
+    starts = dev(list(range(n + 1)), torch.int32)
+
+    def run(lens):
+        b = c.cache.batch(table, dev(lens, torch.int32), starts, total_rows=n, max_rows=1, max_len=longest)
+        out, lse = torch.full_like(q, 7.0), torch.full((n, H * G), 7.0, device="cuda")
+        c.cache.attention(b, q, out=out, lse=lse, status=c.status)
+        return out, lse
+
+    out, lse = run(lens)
+    assert c.status.item() == 0
+    c.lens, c.starts, c.table = lens, list(range(n + 1)), c.table * n
+    check_attention(c, q, out, lse, D ** -0.5, True, f"{n} sequences")
+    bad = {5: -3, 11: longest + 1, 20: -2 ** 31, 21: 2 ** 31 - 1}
+    got, _ = run([bad.get(z, x) for z, x in enumerate(lens)])
+    assert c.status.item() == 1 << kvtc.ERR_INVALID_ARG
+    for z in range(n):
+        assert (got[z] == 7.0).all() if z in bad else torch.equal(got[z], out[z]), z
+
+
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 8.0])
 def test_attention_scales(scale):
     """Flat and needle-sharp weights, scores that grow along the sequence."""
@@ -565,7 +595,7 @@ def test_pool_offsets_past_32_bits():
         cache.write(batch(ln), k, v, layer=1, status=c.status)
         ko, vo = torch.empty_like(k), torch.empty_like(v)
         cache.read(batch(ln), ko, vo, layer=1, status=c.status)
-        outs = [cache.pool[1, table[0].long()], ko, vo]
+        outs = [cache.pool[1, table[0, :ln // 16].long()], ko, vo]  # (the last page is not full: anything behind its tokens)
         for rows in (2, 17, 200):
             q = k[:rows].repeat(1, 2, 1) + v[:rows].repeat(1, 2, 1)
             outs.append(cache.attention(batch(rows), q, layer=1, status=c.status))
