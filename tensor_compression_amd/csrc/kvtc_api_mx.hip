@@ -68,11 +68,11 @@ bool bad_strides(const int64_t* st, const int64_t (&extent)[3], int D, int elem,
   std::pair<int64_t, int64_t> d[3];
   for (int i = 0; i < 3; ++i) d[i] = {st[i], extent[i]};
   std::sort(d, d + 3);
-  int64_t span = D;
+  __int128 span = D;  // 2^46 by 2^31 rows passes 64 bits
   for (const auto& [s, n] : d) {
     if (n < 2) continue;
     if (s < span) return true;
-    span += s * (n - 1);
+    span += (__int128)s * (n - 1);
   }
   return false;
 }

@@ -170,6 +170,15 @@ def test_overlapping_outputs():
     assert call("read", n_layers=2, ks=strides(0, 128, 512)) == INV
 
 
+def test_overlapping_outputs_of_huge_strides():
+    """Spans past 64 bits: row 1 of layer 0 and row 0 of layer 1 lie 8 elements apart."""
+    b = batch(n_seqs=0, total_rows=2 ** 31 - 1)
+    for rows, layers in ((2 ** 34, 2 ** 34 + 8), (2 ** 33, 2 ** 46), (2 ** 46, 2 ** 46)):
+        assert call("read", b=b, n_layers=2, ks=strides(layers, 128, rows)) == INV
+        assert call("read", b=b, n_layers=2, ks=strides(layers, 128, 512), vs=strides(layers, 128, rows)) == INV
+    assert call("read", b=b, n_layers=2, ks=strides(2 ** 45, 128, 512), vs=strides(2 ** 45, 128, 512)) == kvtc.OK
+
+
 @pytest.mark.parametrize("name", ["attn", "shared"])
 def test_bad_attention(name):
     for bad in (dict(q=None), dict(out=None), dict(q=P + 2), dict(out=P + 8), dict(lse=P + 2), dict(ws=P + 8),
