@@ -598,6 +598,8 @@ class MxCache:
             pool = torch.empty(shape, dtype=torch.uint8, device=device)
         if pool.dtype != torch.uint8 or tuple(pool.shape) != shape or not pool.is_contiguous():
             raise ValueError(f"the pool is a contiguous uint8 tensor of shape {shape}")
+        if not pool.is_cuda:
+            raise ValueError(f"a pool on {pool.device}: the kernels read and write it on a GPU")
         self.pool, self.pool_pages, self.device = pool, pool_pages, pool.device
         self._index = pool.get_device()
         self._strides = {}

@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import mx_ref
 from tensor_compression_amd import kvtc
@@ -211,6 +212,15 @@ def test_grid_of_both_passes():
             assert call("shared", c=c, b=b, q_heads=1) == want
     b = batch(n_seqs=most, total_rows=4096, max_rows=1)
     assert kvtc.lib().kvtc_mx_attn_workspace(ctypes.byref(c), ctypes.byref(b), 1, 0, ctypes.byref(n)) == kvtc.OK
+
+
+def test_a_pool_in_host_memory_is_refused():
+    """The kernels would follow a host pointer."""
+    c = dict(layers=1, kv_heads=2, head_dim=64, dtype=kvtc.BF16, bits_k=4, bits_v=4)
+    with pytest.raises(ValueError):
+        kvtc.MxCache(c, 3, device="cpu")
+    with pytest.raises(ValueError):
+        kvtc.MxCache(c, 3, pool=torch.empty(1, 3, 2, mx_ref.record_bytes(64, 4, 4), dtype=torch.uint8))
 
 
 @pytest.mark.parametrize("name", CALLS)
