@@ -619,6 +619,8 @@ class MxCache:
 
     def _call(self, fn, stream, *args):
         """Runs a library call with the cache's device current."""
+        if stream is not None and stream.device_index != self._index:
+            raise ValueError(f"a stream of device {stream.device_index} for a cache on {self.device}")
         if torch.cuda.current_device() == self._index:
             st = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(self._index))
         else:

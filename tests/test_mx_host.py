@@ -1,6 +1,7 @@
 """The microscaled paged cache on the CPU: the plain implementation's own
 pins, and what the library refuses before anything is launched."""
 import ctypes
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -221,6 +222,15 @@ def test_a_pool_in_host_memory_is_refused():
         kvtc.MxCache(c, 3, device="cpu")
     with pytest.raises(ValueError):
         kvtc.MxCache(c, 3, pool=torch.empty(1, 3, 2, mx_ref.record_bytes(64, 4, 4), dtype=torch.uint8))
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Before anything is launched on it."""
+    cache, ran = object.__new__(kvtc.MxCache), []
+    cache._index, cache.device = 0, torch.device("cuda", 0)
+    with pytest.raises(ValueError):
+        cache._call(lambda *a: ran.append(a), SimpleNamespace(device_index=1, cuda_stream=0))
+    assert not ran
 
 
 @pytest.mark.parametrize("name", CALLS)
