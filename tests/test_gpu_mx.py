@@ -704,3 +704,168 @@ def test_decoded_cache_is_served_and_encoded_again():
     assert st == kvtc.OK and c.status.item() == 0
     k2, v2, st = plan.decode(data, total, kvtc.BF16)
     assert st == kvtc.OK and torch.equal(k2[:, :, -32:], ko[:, :, -32:])
+
+
+# ---- every kernel in every format, batches of unlike sequences, captured ranges
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+@pytest.mark.parametrize("D,bk,bv", FORMATS)
+def test_attention_many_rows_formats(D, bk, bv, dtype):
+    """The kernel for many rows in every format: prompts with and without
+    tokens before them, a lone row and a sequence without rows among them."""
+    rows, lens = [150, 1, 0, 70, 129], [150, 260, 40, 70, 300]
+    for G, causal in ((2, True), (3, False)):
+        c = Case(D, bk, bv, dtype, 2, rows, lens, seed=D + 2 * bk + bv, total_rows=sum(rows) + 2)
+        c.fill()
+        q, out, lse, scale = run_attention(c, G, causal)
+        check_attention(c, q, out, lse, scale, causal, f"many rows D{D} k{bk} v{bv} dtype {dtype} causal {causal}")
+
+
+@pytest.mark.parametrize("most", [2, 7, 40])
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+@pytest.mark.parametrize("D,bk,bv", FORMATS)
+def test_attention_behind_a_prefix_formats(D, bk, bv, dtype, most):
+    """More than 64 rows together behind a prefix, in every format: a few own
+    rows a sequence (both passes in one launch), some, and many."""
+    rng = np.random.default_rng(D + bk + bv + most)
+    n = 30 if most < 40 else 4
+    lens = [160 + int(x) for x in rng.integers(0, 150, n)]
+    lens[0], lens[1], lens[n - 1] = 160, 90, 161
+    rows = [1 + int(x) for x in rng.integers(0, most, n)]
+    rows[2], rows[3] = most, 0
+    c = Case(D, bk, bv, dtype, 2, rows, lens, seed=most, shared=10, total_rows=sum(rows) + 1)
+    c.fill()
+    for causal in (True, False):
+        q, out, lse, scale = run_attention(c, 3, causal, shared=10)
+        check_attention(c, q, out, lse, scale, causal, f"behind D{D} k{bk} v{bv} dtype {dtype} rows {most} causal {causal}")
+
+
+@pytest.mark.parametrize("D,bk,bv,dtype,H,shared", [(64, 4, 4, kvtc.BF16, 8, 1100), (64, 8, 4, kvtc.FP32, 8, 1100),
+                                                    (128, 4, 4, kvtc.BF16, 4, 2200)])
+def test_attention_few_rows_behind_a_long_prefix(D, bk, bv, dtype, H, shared):
+    """At most 16 rows together: ranges of the prefix long enough for the
+    larger workgroups, a sequence inside the prefix, one at its end."""
+    p = 16 * shared
+    lens = [p + 5, p, p + 300, p - 7000, 40]
+    c = Case(D, bk, bv, dtype, H, [1, 1, 2, 1, 1], lens, seed=D + bk, shared=shared, total_rows=8)
+    c.fill()
+    q, out, lse, scale = run_attention(c, 2, shared=shared)
+    check_attention(c, q, out, lse, scale, True, f"long prefix D{D} k{bk} v{bv} dtype {dtype}")
+
+
+@pytest.mark.parametrize("rows,G", [(1, 20), (5, 4), (1, 32)])
+def test_attention_sequences_by_length_of_some_rows(rows, G):
+    """More whole sequences than compute units take, in tiles of 32 rows, in
+    part and all full."""
+    n, H, D = 36, 8, 64
+    lens = [int(x) for x in np.random.default_rng(G).integers(0, 2101, n)]
+    lens[0], lens[5], lens[6], lens[7] = 2100, 0, 1, 2100
+    c = Case(D, 8, 4, kvtc.BF16, H, [1], [2100], seed=G)
+    c.fill()
+    c.table_dev, c.table = c.table_dev.expand(n, -1).contiguous(), c.table * n
+    take = [rows if z % 3 else max(rows - 1, 0) for z in range(n)]
+    c.lens, c.rows, c.starts, c.total = lens, take, [0] + [int(x) for x in np.cumsum(take)], sum(take) + 1
+    c.batch = c.new_batch(take, lens, max_rows=rows)
+    q, out, lse, scale = run_attention(c, G)
+    check_attention(c, q, out, lse, scale, True, f"by length {rows} rows of {G}")
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_prompts_beside_single_rows(dtype, causal):
+    """One call for a prompt's chunk and the decode steps of the others: some
+    long, some empty, some with more rows than tokens (which see no token when
+    causal, and all of them when not)."""
+    lens = [400, 1, 0, 17, 900, 2, 33, 64, 5, 1500] + [100 + 13 * z for z in range(12)]
+    rows = [130, 1, 1, 1, 1, 5, 1, 0, 9, 2] + [1] * 12
+    for D, bk, bv in ((128, 4, 4), (64, 8, 8)):
+        c = Case(D, bk, bv, dtype, 2, rows, lens, seed=D, total_rows=sum(rows) + 4)
+        c.fill()
+        q, out, lse, scale = run_attention(c, 4, causal)
+        check_attention(c, q, out, lse, scale, causal, f"mixed D{D} dtype {dtype} causal {causal}")
+
+
+@pytest.mark.parametrize("rows", [2, 20, 80])
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_attention_scores_up_to_their_bound(dtype, rows):
+    """Scores of up to 2^25 of either sign and values of 2^64.  Keys of one
+    channel and a query of one power of two: products and scores are exact and
+    at least 2^16 apart, so a row is the mean of the tokens with its largest score, and
+    its log-sum-exp that score and the logarithm of their number."""
+    D, ln = 64, 300
+    u = 2.0 ** -8 if dtype == kvtc.BF16 else 2.0 ** -23
+    for sign in (1.0, -1.0):
+        for order in ("up", "down", "mixed"):
+            c = Case(D, 8, 8, dtype, 1, [rows], [ln], seed=rows)
+            t = {"up": np.arange(ln), "down": np.arange(ln)[::-1].copy(), "mixed": c.rng.permutation(ln)}[order] // 7
+            lead = (8 + t % 8) * 2.0 ** (t // 8)  # 42 values with four significant bits, 8 to 320
+            k, v = torch.zeros(ln, 1, D, dtype=DT[dtype], device="cuda"), c.rand(ln, 1, D) * 2.0 ** 60
+            v = v.clamp(-2.0 ** 64, 2.0 ** 64)
+            k[:, 0, 0] = dev(lead, torch.float32).to(DT[dtype])
+            b = c.new_batch([ln], [ln], total_rows=ln)
+            c.cache.write(b, k, v, status=c.status)
+            q = torch.zeros(rows, 2, D, dtype=DT[dtype], device="cuda")
+            q[:, :, 0] = sign * 2.0 ** 10
+            lse = torch.empty(rows, 2, device="cuda")
+            out, _ = c.cache.attention(c.batch, q, 2.0 ** 6, lse=lse, status=c.status)
+            score = sign * 2.0 ** 16 * lead
+            assert np.abs(score).max() < 2.0 ** 25
+            vp = mx_ref.tokens(*c.unpacked(), c.table[0], ln)[1][0]
+            for i in range(rows):
+                lim = ln - rows + i + 1
+                top = score[:lim] == score[:lim].max()
+                want = vp[:lim][top].mean(0)
+                # weights and output are rounded once each, the sum of the few weights by as many steps of 2^-24
+                tol = 2 * u * np.abs(vp[:lim][top]).mean(0) + 64 * 2.0 ** -24 * np.abs(vp[:lim][top]).max()
+                assert (np.abs(np64(out)[i] - want) <= tol).all(), (sign, order, i)
+                wl = score[:lim].max() + np.log(top.sum())
+                # roundings of scale log2(e), of the sum, of ln 2, of their product and of the join
+                assert (np.abs(np64(lse)[i] - wl) <= 5 * 2.0 ** -24 * abs(wl)).all(), (sign, order, i)
+    assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_captured_ranges_follow_lengths_and_rows(dtype):
+    """A call captured under bounds that split the tokens into ranges, replayed
+    while lengths cross the ranges' borders, rows move between the sequences
+    and one of them has none; every replay against the plain implementation
+    and against the eager call, rows of no sequence left alone."""
+    D, H, G, n, most = 64, 2, 2, 4, 3000
+    c = Case(D, 8, 4, dtype, H, [1] * n, [most] * n, seed=44, shared=8, total_rows=9)
+    c.fill()
+    lens, starts = dev([1] * n, torch.int32), dev([0] * (n + 1), torch.int32)
+    b = c.cache.batch(c.table_dev, lens, starts, total_rows=9, max_rows=4, max_len=most)
+    q = c.rand(9, H * G, D)
+    outs = [torch.empty_like(q) for _ in range(2)]
+    lses = [torch.empty(9, H * G, device="cuda") for _ in range(2)]
+    ws = [c.cache.workspace(b, H * G), c.cache.workspace(b, H * G, 8)]
+    assert all(w.nbytes > 16 for w in ws)
+
+    def step(o, s):
+        c.cache.attention(b, q, out=o[0], lse=s[0], ws=ws[0], status=c.status)
+        c.cache.attention_shared(b, q, 8, out=o[1], lse=s[1], ws=ws[1], status=c.status)
+
+    step(outs, lses)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(outs, lses)
+    for r, (ln, rows) in enumerate([((128, 129, 127, 1), (1, 1, 1, 1)), ((3000, 256, 2999, 130), (4, 0, 2, 1)),
+                                    ((0, 5, 128, 2177), (1, 3, 0, 4)), ((64, 1000, 2048, 257), (0, 0, 4, 0)),
+                                    ((2945, 2944, 2943, 40), (2, 2, 2, 3)), ((128, 129, 127, 1), (1, 1, 1, 1))]):
+        c.lens, c.starts = list(ln), [0] + [int(x) for x in np.cumsum(rows)]
+        lens.copy_(dev(c.lens, torch.int32))
+        starts.copy_(dev(c.starts, torch.int32))
+        q.copy_(c.rand(9, H * G, D))
+        for x in (*outs, *lses):
+            x.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        e, es = [torch.full_like(x, 7.0) for x in outs], [torch.full_like(x, 7.0) for x in lses]
+        step(e, es)
+        for o, s, o2, s2 in zip(outs, lses, e, es):
+            assert torch.equal(o, o2) and torch.equal(s, s2), r
+            assert (o[c.starts[-1]:] == 7.0).all() and (s[c.starts[-1]:] == 7.0).all(), r
+            check_attention(c, q, o, s, D ** -0.5, True, f"replay {r} dtype {dtype}")
+    assert c.status.item() == 0
