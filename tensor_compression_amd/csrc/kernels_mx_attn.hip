@@ -1167,7 +1167,7 @@ void launch_pass(const MxAttnParams& p, hipStream_t s) {
 }
 template <int D, int BK, int BV, bool F32>
 hipError_t launch_format(const MxAttnParams* prefix, const MxAttnParams* own, hipStream_t s) {
-  if (prefix && own && prefix->nt == 8 && own->nt == 1 && own->waves == 4 && !own->once) {
+  if (prefix && own && own->together) {
     const unsigned n = blocks_of(*prefix);
     k_mx_both<D, BK, BV, F32><<<n + blocks_of(*own), 256, 0, s>>>(*prefix, *own, (int)n);
     return hipGetLastError();

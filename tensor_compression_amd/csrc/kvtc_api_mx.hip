@@ -149,6 +149,8 @@ Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span) {
 struct AttnPlan {
   Cut prefix, own;  // nsplit 0: no such pass
   int begin;        // first token of `own`
+  bool once;        // `own` reads its codes past the caches
+  bool together;    // both in one launch
   int64_t slots, ws;
 };
 
@@ -162,9 +164,25 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   a->begin = (int)std::min<int64_t>((int64_t)shared * KVTC_MX_PAGE, b.max_len);
   const int64_t rows = (int64_t)std::min(b.max_rows, b.total_rows) * G;
   if (a->begin < b.max_len || a->begin == 0) a->own = cut_pass(rows, b.n_seqs, c.kv_heads, b.max_len - a->begin);
+  // at most this many bytes of codes, against the 256 MB of the memory-side cache
+  a->once = (int64_t)b.n_seqs * (b.max_len - a->begin) / KVTC_MX_PAGE * c.kv_heads *
+                mx_record(c.head_dim, c.bits_k, c.bits_v).bytes > ((int64_t)256 << 20);
   if (a->begin > 0) {
-    a->own.waves = 4;  // beside the prefix's workgroups
     a->prefix = cut_pass((int64_t)b.total_rows * G, 1, c.kv_heads, a->begin);
+    // One launch where the prefix takes the kernel for many rows and the own
+    // tokens the one for few (64 sequences of 1000 own tokens behind 2048: 40
+    // us one after the other, 29 together; 128 of 1800 behind 8192: 100 and
+    // 98).  Codes past the caches go one after the other: the shared kernel's
+    // registers leave the own tokens 2 waves a SIMD instead of 3 (4 bits: 64
+    // of 8000 behind 32768 173 us together, 156 so, 128 of 4000 behind 8192
+    // 158 and 145; 8 bits, with half the instructions a byte, would take it
+    // the other way behind short prefixes: 64 of 4000 behind 8192 121 and 136,
+    // behind 32768 171 and 167).  Four waves a workgroup beside the prefix's
+    // (20 of 4000 behind 8192: 41 us, in a launch of eight 51), otherwise as
+    // `cut_pass` says (8 of 16000 behind 1024: 48 -> 42 us, 24 of 16000 behind
+    // 8192: 140 -> 103).
+    a->together = a->prefix.nt == 8 && a->own.nt == 1 && !a->once;
+    if (a->together) a->own.waves = 4;
   }
   a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
@@ -236,9 +254,8 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   if (!a.prefix.nsplit && a.own.nt < 8 && a.own.tiles == 1 && a.own.nsplit == 1 && b->n_seqs > per_round &&
       b->n_seqs <= 256 && b->max_len >= 2048)
     p.pair = (int32_t)per_round;
-  // at most this many bytes of codes, against the 256 MB of the memory-side cache
-  p.once = (int64_t)b->n_seqs * (b->max_len - a.begin) / KVTC_MX_PAGE * cfg->kv_heads *
-               mx_record(cfg->head_dim, cfg->bits_k, cfg->bits_v).bytes > ((int64_t)256 << 20);
+  p.once = a.once;
+  p.together = a.together;
   if (launch_mx_attn(a.prefix.nsplit ? &prefix : nullptr, a.own.nsplit ? &p : nullptr, cfg->head_dim, cfg->bits_k,
                      cfg->bits_v, f32, stream) != hipSuccess)
     return KVTC_ERR_HIP;

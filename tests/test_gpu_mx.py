@@ -869,3 +869,22 @@ def test_captured_ranges_follow_lengths_and_rows(dtype):
             assert (o[c.starts[-1]:] == 7.0).all() and (s[c.starts[-1]:] == 7.0).all(), r
             check_attention(c, q, o, s, D ** -0.5, True, f"replay {r} dtype {dtype}")
     assert c.status.item() == 0
+
+
+@pytest.mark.parametrize("D,bk,bv,dtype", [(128, 4, 4, kvtc.BF16), (64, 8, 8, kvtc.FP32)])
+def test_attention_one_workgroup_a_unit_behind_a_prefix(D, bk, bv, dtype):
+    """Own tokens for the larger workgroups in a launch after the prefix's: the
+    rows together fit one of its tiles or many, under bounds of hundreds of
+    megabytes of codes too."""
+    H, ln = 8, 1500
+    lens = [1500 - 29 * z for z in range(24)] + [0, 48, 49, 20, 303, 304]
+    n = len(lens)
+    for G, bounds in ((2, (1500, 12800)), (4, (1500, 12800))):
+        c = Case(D, bk, bv, dtype, H, [1], [ln], seed=D + G)
+        c.fill()
+        c.table_dev = torch.cat([c.table_dev.expand(n, -1), torch.full((n, 720), 2 ** 30, dtype=torch.int32, device="cuda")], 1)
+        c.table, c.rows, c.lens, c.starts, c.total = c.table * n, [1] * n, lens, list(range(n + 1)), n + 1
+        for bound in bounds:
+            c.batch = c.new_batch(c.rows, lens, max_len=bound)
+            q, out, lse, scale = run_attention(c, G, shared=3)
+            check_attention(c, q, out, lse, scale, True, f"D{D} G{G} bound {bound}")
