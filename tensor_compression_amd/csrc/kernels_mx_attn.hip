@@ -37,7 +37,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 namespace {
 
-constexpr float kLow = -3.0e38f;  // running maximum of a row that has seen nothing
+constexpr float kLow = -3.0e38f;  // running maximum (scaled) of a row that has seen nothing; its first score moves it
 constexpr float kSlack = 8.0f;    // growth (in powers of two) that leaves the maximum as it is
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -281,7 +281,8 @@ struct Softmax {
   __device__ __forceinline__ Softmax() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t] = raise[t] = kLow;
+      m[t] = kLow;
+      raise[t] = -INFINITY;
       l[t] = 0.f;
     }
   }
@@ -884,7 +885,7 @@ __device__ __forceinline__ void many_rows(const MxAttnParams& p, int block, Many
   };
 
   f32x16_t acc[CT], sa;
-  float m = kLow, l = 0.f, raise = kLow;
+  float m = kLow, l = 0.f, raise = -INFINITY;
   const float inv_c = 1.0f / p.c;
   uint32_t poison = 0;  // bit b: a value of channel block b was NaN at a token that the lane's row attends to
 #pragma unroll

@@ -888,3 +888,24 @@ def test_attention_one_workgroup_a_unit_behind_a_prefix(D, bk, bv, dtype):
             c.batch = c.new_batch(c.rows, lens, max_len=bound)
             q, out, lse, scale = run_attention(c, G, shared=3)
             check_attention(c, q, out, lse, scale, True, f"D{D} G{G} bound {bound}")
+
+
+@pytest.mark.parametrize("rows", [2, 20, 80])
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_attention_products_near_the_end_of_fp32(dtype, rows):
+    """Products of -3.2e38, -2.8e38 and -1.6e38 under a scale that makes them
+    ordinary scores, the least ones alone, first, last and in between."""
+    D, ln = 64, 150
+    for order in (np.full(ln, 120.0), np.where(np.arange(ln) < 70, 120.0, 104.0), np.where(np.arange(ln) < 50, 60.0, 120.0),
+                  np.tile([120.0, 104.0, 120.0, 120.0, 60.0], 30)):
+        c = Case(D, 8, 8, dtype, 1, [rows], [ln], seed=rows)
+        k, v = torch.zeros(ln, 1, D, dtype=DT[dtype], device="cuda"), c.rand(ln, 1, D)
+        k[:, 0, 5] = dev(order * 2.0 ** 58, torch.float32).to(DT[dtype])
+        c.cache.write(c.new_batch([ln], [ln], total_rows=ln), k, v, status=c.status)
+        q = torch.zeros(rows, 2, D, dtype=DT[dtype], device="cuda")
+        q[:, :, 5] = -2.0 ** 63
+        lse = torch.empty(rows, 2, device="cuda")
+        for scale in (2.0 ** -124, 2.0 ** -126):
+            out, _ = c.cache.attention(c.batch, q, scale, lse=lse, status=c.status)
+            check_attention(c, q, out, lse, scale, True, f"products {order[:3]} scale {scale}")
+    assert c.status.item() == 0
