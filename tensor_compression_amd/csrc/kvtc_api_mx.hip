@@ -164,9 +164,10 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   a->begin = (int)std::min<int64_t>((int64_t)shared * KVTC_MX_PAGE, b.max_len);
   const int64_t rows = (int64_t)std::min(b.max_rows, b.total_rows) * G;
   if (a->begin < b.max_len || a->begin == 0) a->own = cut_pass(rows, b.n_seqs, c.kv_heads, b.max_len - a->begin);
-  // at most this many bytes of codes, against the 256 MB of the memory-side cache
-  a->once = (int64_t)b.n_seqs * (b.max_len - a->begin) / KVTC_MX_PAGE * c.kv_heads *
-                mx_record(c.head_dim, c.bits_k, c.bits_v).bytes > ((int64_t)256 << 20);
+  // at most this many bytes of codes (past 64 bits in calls that are refused
+  // below), against the 256 MB of the memory-side cache
+  a->once = (double)b.n_seqs * (b.max_len - a->begin) / KVTC_MX_PAGE * c.kv_heads *
+                mx_record(c.head_dim, c.bits_k, c.bits_v).bytes > 0x1p28;
   if (a->begin > 0) {
     a->prefix = cut_pass((int64_t)b.total_rows * G, 1, c.kv_heads, a->begin);
     // One launch where the prefix takes the kernel for many rows and the own
