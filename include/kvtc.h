@@ -536,8 +536,9 @@ kvtc_status kvtc_pq_decode(kvtc_plan_t plan, const kvtc_pq_config* q, const floa
  * power-of-two scale (E8M0) per token, head and 32 channels.
  *
  * Quantising a block of 32 channels with a = max|x|: the scale is 2^e with
- * the smallest e for which a rounds to a finite element, a < 7 2^e (E2M1,
- * largest element 6) or a < 464 2^e (E4M3, 448), e clamped to [-112, 125]
+ * the smallest e for which a lies less than half a step past the largest
+ * element: a < 7 2^e (E2M1, 6 and a step of 2) or a < 464 2^e (E4M3, 448 and
+ * a step of 32; a = 464 2^e itself takes the next e), e clamped to [-112, 125]
  * (E2M1) or [-112, 119] (E4M3); elements are x 2^-e rounded to nearest even,
  * saturating at the clamp.  So no element is off by more than half a step of
  * its grid, and every value of the cache is a bf16 number.  A block with a
@@ -562,11 +563,18 @@ kvtc_status kvtc_pq_decode(kvtc_plan_t plan, const kvtc_pq_config* q, const floa
  * step that appends one token has one row a sequence, a prompt has all of
  * them, and kv_lens counts the tokens after the write.  A sequence may have
  * no rows; positions below 0 (more rows than tokens) are skipped when
- * writing and reading, and are empty rows of the attention.  Tensor rows
- * that belong to no sequence are left as they are.
+ * writing and reading, and are empty rows of the causal attention.  Tensor
+ * rows that belong to no sequence are left as they are.
  *
  * The three arrays are device memory and only the bounds are the host's, so
  * a captured call can be replayed with other lengths and pages within them.
+ * The bounds also decide how an attention call is cut up, so its time follows
+ * them: ranges of max_len tokens that a short sequence leaves empty are
+ * workgroups without work (one sequence of 4096 tokens: 9 us under a bound of
+ * 4096, 22 under 131072), and max_rows picks one kernel for the whole batch
+ * (a prompt of 2048 rows beside 63 decode steps: 633 us in one call, 220 in
+ * two).  A step captured once per range of lengths and calls of their own for
+ * prompts and decode steps avoid both.
  * The device checks what it reads: a length or row range outside the bounds
  * makes the call skip that sequence, a page index outside the pool skips
  * that page's tokens (the attention takes them as masked), and either sets
@@ -638,12 +646,15 @@ kvtc_status kvtc_mx_attn_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batc
  * h head_dim.  out: device [total_rows, q_heads, head_dim] in cfg->dtype;
  * lse: device fp32 [total_rows, q_heads] or NULL.  A row that attends to
  * nothing gets zeros and lse -infinity.  scale must be a positive normal
- * number, at most 2^100.
+ * number, at most 2^100.  Scores may reach 2^25 of either sign, products
+ * q . k the end of fp32, queries the largest bf16 number and values 2^64.
+ * What lies further out (scores that fp32 sums no longer tell apart, sums
+ * that overflow) may give NaN or zeros in the rows that meet it.
  * A NaN token affects the rows that attend to it and no others.
  *
  * Products are exact (bf16 queries) and summed in fp32, the softmax is fp32;
  * the weights are rounded to bf16 before they meet the values, as the output
- * is.  fp32 queries and weights are split into three bf16 parts that keep
+ * is (an error of 2^-8 each of the terms' and the output's magnitude).  fp32 queries and weights are split into three bf16 parts that keep
  * 24 bits.  Deterministic. */
 kvtc_status kvtc_mx_attn(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,
                          size_t pool_bytes, const void* q, int64_t q_stride, int32_t q_heads, float scale,

@@ -40,8 +40,9 @@ __device__ __forceinline__ uint32_t block_max(uint32_t a) {
 }
 
 // Scale byte of a block whose largest magnitude has the bits a: the exponent
-// of a less that of the largest element, one more where the mantissa of a
-// would round past it (1.75 of 2 for 6 -> 8, 1.8125 for 448 -> 480).
+// of a less that of the largest element, one more where the mantissa of a is
+// half a step past it or further (1.75, between 6 and 8; 1.8125, between 448
+// and where 480 would be).
 template <int B>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t a) {
   const int up = (a & 0x7FFFFFu) >= (B == 4 ? 0x600000u : 0x680000u);
