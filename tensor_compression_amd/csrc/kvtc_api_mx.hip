@@ -140,8 +140,9 @@ Cut cut_pass(int64_t rows, int64_t seqs, int H, int64_t span) {
   c.chunk = (int)(((span + n - 1) / n + 127) / 128 * 128);
   c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / std::max(c.chunk, 1));
   // Eight waves where a CU has one workgroup with enough for all of them (24
-  // sequences of 16000 tokens: 114 -> 79 us); beside others, or with little
-  // to do, four (40 of 4000: 34 us, eight 40; 1 of 8000 in 256s: 8.7 and 9.0).
+  // sequences of 16000 tokens: 114 -> 79 us; the prefix of 4 sequences behind
+  // 131072: 47 -> 41); beside others, or with little to do, four (40 of 4000:
+  // 34 us, eight 40; 1 of 8000 in 256s: 8.7 and 9.0).
   c.waves = c.nt == 1 && units <= 256 && c.chunk > 512 ? 8 : 4;
   return c;
 }
@@ -248,9 +249,10 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   p.fold = causal && a.own.nt == 8 && a.own.tiles * cfg->kv_heads * a.own.nsplit * b->n_seqs <= 512;
   // Whole sequences, more workgroups than compute units: first the longest, one
   // a unit and in rising order, then the others from the longest on, so that
-  // the second of a unit makes up for its first (sequences of 511 to 8191 tokens, 8 heads: 64 of
-  // them 67 -> 62 us, 128 115 -> 94; all of 4000: 64 46.7 -> 47.7, so not where
-  // they are short).
+  // the second of a unit makes up for its first (sequences of 511 to 8191
+  // tokens, 8 heads: 64 of them 67 -> 62 us, 128 115 -> 94, with 5 rows each
+  // 89 -> 79 and 146 -> 120; all of 4000: 64 46.7 -> 47.7, so not where they
+  // are short).
   const int64_t per_round = std::max(256 / cfg->kv_heads, 1);
   if (!a.prefix.nsplit && a.own.nt < 8 && a.own.tiles == 1 && a.own.nsplit == 1 && b->n_seqs > per_round &&
       b->n_seqs <= 256 && b->max_len >= 2048)
