@@ -188,8 +188,8 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   }
   a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
-  // (both passes together: they may share a launch)
-  if ((a->own.tiles * a->own.nsplit * b.n_seqs + a->prefix.tiles * a->prefix.nsplit) * c.kv_heads > kMaxGrid ||
+  if (a->own.tiles * c.kv_heads * std::max(a->own.nsplit, 1) * b.n_seqs > kMaxGrid ||
+      a->prefix.tiles * c.kv_heads * std::max(a->prefix.nsplit, 1) > kMaxGrid ||
       (int64_t)b.total_rows * q_heads > 4 * kMaxGrid)
     return KVTC_ERR_UNSUPPORTED;
   return KVTC_OK;

@@ -200,21 +200,6 @@ def test_bad_prefix_and_workspace():
     assert call("shared", ws_bytes=n.value - 1) == CAP and call("shared", ws=None) == INV
 
 
-def test_grid_of_both_passes():
-    """A prefix and the sequences' own tokens, each within a launch's
-    workgroups and together past them; one sequence less would fit."""
-    c, n = cfg(kv_heads=1), ctypes.c_size_t(0)
-    most = 2 ** 24 - 1
-    tiles = -(-4096 // 128)
-    for seqs, want in ((most - tiles, kvtc.OK), (most - tiles + 1, UNS), (most, UNS)):
-        b = batch(n_seqs=seqs, total_rows=4096, max_rows=1)
-        assert kvtc.lib().kvtc_mx_attn_workspace(ctypes.byref(c), ctypes.byref(b), 1, 2, ctypes.byref(n)) == want
-        if want != kvtc.OK:
-            assert call("shared", c=c, b=b, q_heads=1) == want
-    b = batch(n_seqs=most, total_rows=4096, max_rows=1)
-    assert kvtc.lib().kvtc_mx_attn_workspace(ctypes.byref(c), ctypes.byref(b), 1, 0, ctypes.byref(n)) == kvtc.OK
-
-
 def test_a_pool_in_host_memory_is_refused():
     """The kernels would follow a host pointer."""
     c = dict(layers=1, kv_heads=2, head_dim=64, dtype=kvtc.BF16, bits_k=4, bits_v=4)
