@@ -654,8 +654,9 @@ kvtc_status kvtc_mx_attn_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batc
  *
  * Products are exact (bf16 queries) and summed in fp32, the softmax is fp32;
  * the weights are rounded to bf16 before they meet the values, as the output
- * is (an error of 2^-8 each of the terms' and the output's magnitude).  fp32 queries and weights are split into three bf16 parts that keep
- * 24 bits.  Deterministic. */
+ * is (at most 2^-8 of the terms' and of the output's magnitude).  fp32
+ * queries and weights are split into three bf16 parts that keep 24 bits.
+ * Deterministic. */
 kvtc_status kvtc_mx_attn(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,
                          size_t pool_bytes, const void* q, int64_t q_stride, int32_t q_heads, float scale,
                          int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status_dev,

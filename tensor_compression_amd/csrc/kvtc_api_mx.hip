@@ -188,6 +188,8 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   }
   a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
+  // (each its own launch; in one they have at most 256 MB of own codes, so
+  // fewer than 2^22 workgroups of own tokens, and 2^20 of the prefix)
   if (a->own.tiles * c.kv_heads * std::max(a->own.nsplit, 1) * b.n_seqs > kMaxGrid ||
       a->prefix.tiles * c.kv_heads * std::max(a->prefix.nsplit, 1) > kMaxGrid ||
       (int64_t)b.total_rows * q_heads > 4 * kMaxGrid)

@@ -42,12 +42,12 @@ struct MxAttnParams {
   float* lse;
   int32_t prefix;      // 1: rows of all sequences against the first one's pages
   int32_t begin, end;  // token range of this pass
-  int32_t nt;     // 16-row tiles of a workgroup: 1 or 2 (k_mx_attn), 8 (k_mx_rows)
-  int32_t waves;  // waves of a workgroup: 4, or 8 with nt 1
-  int32_t fold;   // pair long tiles with short ones
+  int32_t nt;        // 16-row tiles of a workgroup: 1 or 2 (k_mx_attn), 8 (k_mx_rows)
+  int32_t waves;     // waves of a workgroup: 4, or 8 with nt 1
+  int32_t fold;      // pair long tiles with short ones
   int32_t once;      // read the codes past the caches (nt 1)
   int32_t together;  // (own tokens) in one launch with the prefix
-  int32_t pair;   // sequences by length, the longest `pair` in rising order, then falling; 0: as they come
+  int32_t pair;      // sequences by length, the longest `pair` in rising order, then falling; 0: as they come
   int32_t tiles, nsplit, chunk;
   int32_t slot0;   // first partial slot of this pass
   float* ws_o;     // [slot][total_rows q_heads][D]

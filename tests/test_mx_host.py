@@ -200,6 +200,17 @@ def test_bad_prefix_and_workspace():
     assert call("shared", ws_bytes=n.value - 1) == CAP and call("shared", ws=None) == INV
 
 
+def test_grids_of_both_passes():
+    """Each pass within a launch's workgroups: planned.  The own tokens' past
+    them: refused."""
+    c, n = cfg(kv_heads=1), ctypes.c_size_t(0)
+    for seqs, want in ((2 ** 24 - 1, kvtc.OK), (2 ** 24, UNS)):
+        b = batch(n_seqs=seqs, total_rows=4096, max_rows=1)
+        for shared in (0, 2):
+            assert kvtc.lib().kvtc_mx_attn_workspace(ctypes.byref(c), ctypes.byref(b), 1, shared, ctypes.byref(n)) == want
+    assert call("shared", c=c, b=b, q_heads=1) == UNS and call("attn", c=c, b=b, q_heads=1) == UNS
+
+
 def test_a_pool_in_host_memory_is_refused():
     """The kernels would follow a host pointer."""
     c = dict(layers=1, kv_heads=2, head_dim=64, dtype=kvtc.BF16, bits_k=4, bits_v=4)
