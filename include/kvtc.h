@@ -672,6 +672,99 @@ kvtc_status kvtc_mx_attn_shared(const kvtc_mx_config* cfg, const kvtc_mx_batch* 
                                 int64_t q_stride, int32_t q_heads, float scale, int32_t causal, void* out, float* lse,
                                 void* ws, size_t ws_bytes, uint32_t* status_dev, hipStream_t stream);
 
+/* ---- microscaled paged cache: rotation on the way in, drafts -------------- */
+
+/* A rotation of row channels by position (RoPE).  Pair j < rot_dim / 2 is
+ * channels (j, j + rot_dim / 2) (KVTC_ROPE_HALF) or (2j, 2j + 1)
+ * (KVTC_ROPE_INTERLEAVED); at position t of its axis it turns by the angle
+ * t freqs[j], the product in fp64:
+ *   (a, b) -> (a cos - b sin, a sin + b cos).
+ * Channels from rot_dim on stay as they are.  Axes (time, height, width ...)
+ * give a row one position each; any assignment of pairs to axes is allowed.
+ * |t freqs[j]| should stay below 2^45, where the angle itself is no longer
+ * known to 2^-8; frequencies that are not finite make NaN rows. */
+typedef struct kvtc_mx_rope {
+  int32_t style;       /* KVTC_ROPE_HALF or KVTC_ROPE_INTERLEAVED */
+  int32_t rot_dim;     /* multiple of 16, at most head_dim */
+  int32_t axes;        /* 1 to 4 */
+  int32_t reserved;    /* 0 */
+  const double* freqs; /* device [rot_dim / 2], radians a unit of position */
+  const uint8_t* axis; /* host [rot_dim / 2], each below axes; NULL: all 0.  Read during the call */
+} kvtc_mx_rope;
+
+/* kvtc_mx_write with the keys rotated on the way, and the queries of the same
+ * rows rotated beside them.  positions: device int32 [axes][total_rows], of
+ * either sign; NULL (one axis only): each row's position in the cache.
+ * Drafts, whose rows do not stand one behind the other, give their own.
+ *
+ * Keys are rotated in fp64 and quantised from there, without a rounding in
+ * between: their codes are those of the exact rotation, but where that comes
+ * within 2^-51 (|a| + |b|) of a rounding border.  Rotated keys past the end of
+ * fp32 saturate.  Values are quantised as kvtc_mx_write does.  Queries are rotated
+ * in fp32 (cos and sin rounded to it from fp64) and rounded once to their
+ * type: element (r, h, c) from q + r q_stride + h head_dim + c to q_out +
+ * r q_out_stride + h head_dim + c.  q_out may be q with the same stride; it
+ * must not overlap the call's inputs otherwise.  q_heads 0: no queries, q and
+ * q_out are not looked at; else n_layers must be 1.  q_stride and
+ * q_out_stride as in kvtc_mx_attn, q_out_stride at least q_heads head_dim.
+ * Queries of rows before the first token (more rows than tokens) are rotated
+ * too, those of a page outside the pool as well.  The status bits are
+ * kvtc_mx_write's; q_out may hold NaN and infinities that q brought. */
+kvtc_status kvtc_mx_write_rope(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                               const kvtc_mx_rope* rope, const int32_t* positions, const void* k,
+                               const int64_t* k_strides, const void* v, const int64_t* v_strides, const void* q,
+                               int64_t q_stride, int32_t q_heads, void* q_out, int64_t q_out_stride, void* pool,
+                               size_t pool_bytes, uint32_t* status_dev, hipStream_t stream);
+
+/* Drafts.  A batch's rows may be drafted tokens, several continuations of a
+ * sequence at once: they lie in the cache one behind the other, as its last
+ * tokens, but each sees only the tokens before the draft and those rows that
+ * its mask names.  A mask is `words` words of 32 bits, bit j % 32 of word j /
+ * 32 for row j of the same sequence; bits from the sequence's rows on are not
+ * looked at.  32 words must be at least max_rows, and max_rows at most
+ * KVTC_MX_MAX_DRAFT, where a call takes masks (INVALID_ARG, UNSUPPORTED). */
+enum { KVTC_MX_MAX_DRAFT = 4096 };
+
+/* Masks and positions of drafts that are trees.  parents: device int32
+ * [total_rows]: the row (of the same sequence, counted from its first) that a
+ * row follows, lower than its own; -1: it follows the last token before the
+ * draft.  Anything else counts as -1 and sets bit KVTC_ERR_INVALID_ARG.
+ * masks: device [total_rows][words]: the row itself and its ancestors.
+ * positions (device int32 [total_rows], may be NULL): kv_lens[z] - n + the
+ * number of ancestors, what kvtc_mx_write_rope takes.  Rows of no sequence
+ * are left as they are.  The page table is not read. */
+kvtc_status kvtc_mx_tree(const kvtc_mx_batch* batch, const int32_t* parents, uint32_t* masks, int32_t words,
+                         int32_t* positions, uint32_t* status_dev, hipStream_t stream);
+
+/* Workspace bytes of kvtc_mx_attn_tree; as kvtc_mx_attn_workspace. */
+kvtc_status kvtc_mx_attn_tree_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t q_heads,
+                                        int32_t shared_pages, size_t* ws_bytes);
+
+/* Attention of drafts: as kvtc_mx_attn_shared (shared_pages 0: no prefix),
+ * but row i of a sequence's n attends to the tokens t < kv_lens[z] - n and to
+ * the tokens kv_lens[z] - n + j of the rows j < n that its mask names (of any
+ * order; itself only if named).  masks: device [total_rows][words]. */
+kvtc_status kvtc_mx_attn_tree(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,
+                              size_t pool_bytes, int32_t shared_pages, const uint32_t* masks, int32_t words,
+                              const void* q, int64_t q_stride, int32_t q_heads, float scale, void* out, float* lse,
+                              void* ws, size_t ws_bytes, uint32_t* status_dev, hipStream_t stream);
+
+/* Keep the accepted part of drafts: of a sequence's n rows the tokens that
+ * the mask of its row nodes[z] names (of a tree: the path to that node) stay,
+ * in their order, as its tokens kv_lens[z] - n, kv_lens[z] - n + 1, ...; the
+ * codes and scales of layers [layer, layer + n_layers) are moved down to
+ * there, bit for bit.  nodes: device int32 [n_seqs]; -1: none stays.
+ * lens_out (device int32 [n_seqs], not kv_lens): the lengths after it.  What
+ * lies behind them in the pool may be anything.  A node outside the rows, a
+ * sequence outside the bounds: reported, nothing moves, and lens_out is
+ * kv_lens[z]; a token whose page, or whose new page, is outside the pool:
+ * reported and left out of the move.  Sequences without rows keep their
+ * length.  Rows before the first token (more rows than tokens) hold no token
+ * and are passed over. */
+kvtc_status kvtc_mx_keep(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                         const uint32_t* masks, int32_t words, const int32_t* nodes, void* pool, size_t pool_bytes,
+                         int32_t* lens_out, uint32_t* status_dev, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

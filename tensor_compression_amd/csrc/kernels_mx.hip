@@ -20,91 +20,11 @@
 // the keys and values of two heads, read 278000 tokens in 252 us; four heads'
 // keys a workgroup 261, four pages of a head 280, heads before pages 272, keys
 // and values in one wave 270.
-#include "mx_internal.h"
+#include "mx_codes.h"
 
 namespace kvtc {
 
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef short s16x2_t __attribute__((ext_vector_type(2)));
-
 namespace {
-
-// Largest value of the lanes that share a 32-channel block (32 / C lanes).
-template <int C>
-__device__ __forceinline__ uint32_t block_max(uint32_t a) {
-  a = max(a, xor16_u32<1>(a));
-  a = max(a, xor16_u32<2>(a));
-  if constexpr (C == 4) a = max(a, xor16_u32<4>(a));
-  return a;
-}
-
-// Scale byte of a block whose largest magnitude has the bits a: the exponent
-// of a less that of the largest element, one more where the mantissa of a is
-// half a step past it or further (1.75, between 6 and 8; 1.8125, between 448
-// and where 480 would be).
-template <int B>
-__device__ __forceinline__ uint32_t scale_byte(uint32_t a) {
-  const int up = (a & 0x7FFFFFu) >= (B == 4 ? 0x600000u : 0x680000u);
-  const int s = (int)(a >> 23) - (B == 4 ? 2 : 8) + up;
-  return (uint32_t)min(max(s, 15), B == 4 ? 252 : 246);
-}
-
-// C elements under scale 2^(s - 127): 4-bit codes in w[0], 8-bit codes four a word.
-template <int B, int C>
-__device__ __forceinline__ void encode(const float (&x)[C], uint32_t s, uint32_t (&w)[2]) {
-  const float sc = __uint_as_float(s << 23);
-  if constexpr (B == 4) {
-    uint32_t o = 0;
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, x[0], x[1], sc, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, x[2], x[3], sc, 1);
-    if constexpr (C == 8) {
-      o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, x[4], x[5], sc, 2);
-      o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, x[6], x[7], sc, 3);
-    }
-    w[0] = o;
-  } else {
-    // the conversion does not saturate; only a clamped scale needs it to
-    const float top = 448.0f * sc;
-#pragma unroll
-    for (int i = 0; i < C / 4; ++i) {
-      s16x2_t o = {0, 0};
-      o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, __builtin_amdgcn_fmed3f(x[4 * i], -top, top),
-                                                   __builtin_amdgcn_fmed3f(x[4 * i + 1], -top, top), sc, false);
-      o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, __builtin_amdgcn_fmed3f(x[4 * i + 2], -top, top),
-                                                   __builtin_amdgcn_fmed3f(x[4 * i + 3], -top, top), sc, true);
-      w[i] = __builtin_bit_cast(uint32_t, o);
-    }
-  }
-}
-
-// Bytes of a lane's C codes.
-template <int B, int C>
-__device__ __forceinline__ void store_codes(uint8_t* d, const uint32_t (&w)[2]) {
-  if constexpr (B * C == 64) *reinterpret_cast<uint2*>(d) = make_uint2(w[0], w[1]);
-  else if constexpr (B * C == 32) *reinterpret_cast<uint32_t*>(d) = w[0];
-  else *reinterpret_cast<uint16_t*>(d) = (uint16_t)w[0];
-}
-template <int B, int C>
-__device__ __forceinline__ void load_codes(const uint8_t* d, uint32_t (&w)[2]) {
-  if constexpr (B * C == 64) {
-    const uint2 u = *reinterpret_cast<const uint2*>(d);
-    w[0] = u.x;
-    w[1] = u.y;
-  } else if constexpr (B * C == 32) w[0] = *reinterpret_cast<const uint32_t*>(d);
-  else w[0] = *reinterpret_cast<const uint16_t*>(d);
-}
-
-// Where lane (token t = 4 kg + t4, entry n) finds its codes and scale in a record.
-template <int D, int B>
-__device__ __forceinline__ int code_at(bool value, int kg, int t4, int n) {
-  constexpr int U = D / 16 * B / 8;  // bytes of a lane's codes
-  return value ? ((kg * 16 + n) * 4 + t4) * U : ((kg * 4 + t4) * 16 + n) * U;
-}
-template <int D>
-__device__ __forceinline__ int scale_at(bool value, int kg, int t4, int blk) {
-  return value ? (kg * (D / 32) + blk) * 4 + t4 : (kg * 4 + t4) * (D / 32) + blk;
-}
 
 // What a wave works on: page `pg` of sequence z, head h, keys or values.
 struct Unit {
@@ -173,26 +93,8 @@ __device__ __forceinline__ void write_page(const MxIoParams& p, const Unit& u, i
 #pragma unroll
   for (int kg = 0; kg < 4; ++kg) {
     float x[C];
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(raw[kg][i]);
-      else x[i] = __uint_as_float((i & 1) ? raw[kg][i / 2] & 0xFFFF0000u : raw[kg][i / 2] << 16);
-      a = max(a, __float_as_uint(x[i]) & 0x7FFFFFFFu);  // magnitudes order as their bits, NaN above infinity
-    }
-    a = block_max<C>(a);
-    const bool nan = a >= 0x7F800000u;
-    uint32_t s = scale_byte<B>(a), w[2];
-    encode<B, C>(x, s, w);
-    if (nan) {
-      s = 255;
-      w[0] = w[1] = 0;
-    }
-    if (on[kg]) {
-      store_codes<B, C>(codes + code_at<D, B>(u.kv, kg, t4, n), w);
-      if (n % (32 / C) == 0) scales[scale_at<D>(u.kv, kg, t4, n / (32 / C))] = (uint8_t)s;
-      bad |= nan;
-    }
+    unpack<T, C>(raw[kg], x);
+    bad |= put_row<D, B>(x, u.kv, codes, scales, kg, t4, n, on[kg]);
   }
   if (bad && p.status) atomicOr(p.status, 1u << KVTC_ERR_NONFINITE);
 }

@@ -77,9 +77,10 @@ bool bad_strides(const int64_t* st, const int64_t (&extent)[3], int D, int elem,
   return false;
 }
 
-kvtc_status io_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t layer, int32_t n_layers, void* k,
-                    const int64_t* ks, void* v, const int64_t* vs, const void* pool, size_t pool_bytes, int32_t dtype,
-                    uint32_t* status, bool write, hipStream_t stream) {
+// Checks of a write or read, and its parameters but for the units.
+kvtc_status io_params(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t layer, int32_t n_layers, void* k,
+                      const int64_t* ks, void* v, const int64_t* vs, const void* pool, size_t pool_bytes, int32_t dtype,
+                      uint32_t* status, bool write, MxIoParams* p) {
   uint8_t* first;
   const kvtc_status st = check_call(cfg, b, layer, n_layers, pool, pool_bytes, status, &first);
   if (st != KVTC_OK) return st;
@@ -88,22 +89,30 @@ kvtc_status io_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t l
   const int elem = dtype == KVTC_BF16 ? 2 : 4;
   if (bad_strides(ks, extent, cfg->head_dim, elem, !write) || bad_strides(vs, extent, cfg->head_dim, elem, !write))
     return KVTC_ERR_INVALID_ARG;
-  if (nothing_to_do(*b)) return KVTC_OK;
-  if (!k || !v || misaligned(k) || misaligned(v)) return KVTC_ERR_INVALID_ARG;
-  MxIoParams p{};
-  p.b = *b;
-  p.H = cfg->kv_heads;
-  p.pool_pages = cfg->pool_pages;
-  p.n_layers = n_layers;
-  p.pool = first;
-  p.layer_bytes = layer_bytes(*cfg);
-  p.x[0] = k;
-  p.x[1] = v;
+  if (!nothing_to_do(*b) && (!k || !v || misaligned(k) || misaligned(v))) return KVTC_ERR_INVALID_ARG;
+  p->b = *b;
+  p->H = cfg->kv_heads;
+  p->pool_pages = cfg->pool_pages;
+  p->n_layers = n_layers;
+  p->pool = first;
+  p->layer_bytes = layer_bytes(*cfg);
+  p->x[0] = k;
+  p->x[1] = v;
   for (int i = 0; i < 3; ++i) {
-    p.st[0][i] = ks[i];
-    p.st[1][i] = vs[i];
+    p->st[0][i] = ks[i];
+    p->st[1][i] = vs[i];
   }
-  p.status = status;
+  p->status = status;
+  return KVTC_OK;
+}
+
+kvtc_status io_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t layer, int32_t n_layers, void* k,
+                    const int64_t* ks, void* v, const int64_t* vs, const void* pool, size_t pool_bytes, int32_t dtype,
+                    uint32_t* status, bool write, hipStream_t stream) {
+  MxIoParams p{};
+  const kvtc_status st =
+      io_params(cfg, b, layer, n_layers, k, ks, v, vs, pool, pool_bytes, dtype, status, write, &p);
+  if (st != KVTC_OK || nothing_to_do(*b)) return st;
   // n rows that start anywhere in a page touch at most ceil((n + 15) / 16) pages
   const int64_t rows = std::min({b->max_rows, b->total_rows, b->max_len});
   const int64_t units = std::max<int64_t>((rows + 2 * KVTC_MX_PAGE - 2) / KVTC_MX_PAGE, 1);
@@ -112,6 +121,30 @@ kvtc_status io_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t l
   const hipError_t e = write ? launch_mx_write(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, dtype == KVTC_FP32, stream)
                              : launch_mx_read(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, dtype == KVTC_FP32, stream);
   return e == hipSuccess ? KVTC_OK : KVTC_ERR_HIP;
+}
+
+kvtc_status check_rope(const kvtc_mx_rope* r, int D, MxRopeParams* p) {
+  if (!r || r->reserved != 0) return KVTC_ERR_INVALID_ARG;
+  if (r->style != KVTC_ROPE_HALF && r->style != KVTC_ROPE_INTERLEAVED) return KVTC_ERR_INVALID_ARG;
+  if (r->rot_dim < 2 || r->rot_dim > D || r->axes < 1 || r->axes > 4) return KVTC_ERR_INVALID_ARG;
+  if (r->rot_dim % 16) return KVTC_ERR_UNSUPPORTED;  // a lane's channels would be of both halves
+  if (!r->freqs || misaligned(r->freqs, 8)) return KVTC_ERR_INVALID_ARG;
+  for (int j = 0; r->axis && j < r->rot_dim / 2; ++j) {
+    if (r->axis[j] >= r->axes) return KVTC_ERR_INVALID_ARG;
+    p->axis[j / 32] |= (uint64_t)r->axis[j] << (2 * (j % 32));
+  }
+  p->freqs = r->freqs;
+  p->rot = r->rot_dim;
+  p->interleaved = r->style == KVTC_ROPE_INTERLEAVED;
+  return KVTC_OK;
+}
+
+// Masks of drafts: [total_rows][words].
+kvtc_status check_masks(const kvtc_mx_batch& b, const uint32_t* masks, int32_t words) {
+  if (words < 1 || (int64_t)words * 32 < b.max_rows) return KVTC_ERR_INVALID_ARG;
+  if (b.max_rows > KVTC_MX_MAX_DRAFT || words > KVTC_MX_MAX_DRAFT / 32) return KVTC_ERR_UNSUPPORTED;
+  if (misaligned(masks, 4) || (!masks && !nothing_to_do(b))) return KVTC_ERR_INVALID_ARG;
+  return KVTC_OK;
 }
 
 // How one pass of the attention is cut up.
@@ -197,8 +230,9 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
   return KVTC_OK;
 }
 
+// masks: rows are drafts (then causal is 0).
 kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t layer, const void* pool,
-                      size_t pool_bytes, int32_t shared, const void* q, int64_t q_stride, int32_t q_heads, float scale,
+                      size_t pool_bytes, int32_t shared, const uint32_t* masks, int32_t words, const void* q, int64_t q_stride, int32_t q_heads, float scale,
                       int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status,
                       hipStream_t stream) {
   uint8_t* first;
@@ -228,6 +262,8 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   p.out = out;
   p.lse = lse;
   p.status = status;
+  p.masks = masks;
+  p.words = words;
   if (a.slots) {
     p.ws_o = (float*)ws;
     p.ws_ml = (float2*)(p.ws_o + a.slots * b->total_rows * q_heads * (int64_t)cfg->head_dim);
@@ -261,8 +297,9 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
     p.pair = (int32_t)per_round;
   p.once = a.once;
   p.together = a.together;
-  if (launch_mx_attn(a.prefix.nsplit ? &prefix : nullptr, a.own.nsplit ? &p : nullptr, cfg->head_dim, cfg->bits_k,
-                     cfg->bits_v, f32, stream) != hipSuccess)
+  const auto launch = masks ? launch_mx_attn_tree : launch_mx_attn;
+  if (launch(a.prefix.nsplit ? &prefix : nullptr, a.own.nsplit ? &p : nullptr, cfg->head_dim, cfg->bits_k, cfg->bits_v,
+             f32, stream) != hipSuccess)
     return KVTC_ERR_HIP;
   if (!a.slots) return KVTC_OK;
   MxJoinParams j{};
@@ -326,7 +363,7 @@ kvtc_status kvtc_mx_attn(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, 
                          size_t pool_bytes, const void* q, int64_t q_stride, int32_t q_heads, float scale,
                          int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status_dev,
                          hipStream_t stream) {
-  return attn_call(cfg, batch, layer, pool, pool_bytes, 0, q, q_stride, q_heads, scale, causal, out, lse, ws, ws_bytes,
+  return attn_call(cfg, batch, layer, pool, pool_bytes, 0, nullptr, 0, q, q_stride, q_heads, scale, causal, out, lse, ws, ws_bytes,
                    status_dev, stream);
 }
 
@@ -334,8 +371,104 @@ kvtc_status kvtc_mx_attn_shared(const kvtc_mx_config* cfg, const kvtc_mx_batch* 
                                 const void* pool, size_t pool_bytes, int32_t shared_pages, const void* q,
                                 int64_t q_stride, int32_t q_heads, float scale, int32_t causal, void* out, float* lse,
                                 void* ws, size_t ws_bytes, uint32_t* status_dev, hipStream_t stream) {
-  return attn_call(cfg, batch, layer, pool, pool_bytes, shared_pages, q, q_stride, q_heads, scale, causal, out, lse,
+  return attn_call(cfg, batch, layer, pool, pool_bytes, shared_pages, nullptr, 0, q, q_stride, q_heads, scale, causal, out, lse,
                    ws, ws_bytes, status_dev, stream);
+}
+
+kvtc_status kvtc_mx_write_rope(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                               const kvtc_mx_rope* rope, const int32_t* positions, const void* k,
+                               const int64_t* k_strides, const void* v, const int64_t* v_strides, const void* q,
+                               int64_t q_stride, int32_t q_heads, void* q_out, int64_t q_out_stride, void* pool,
+                               size_t pool_bytes, uint32_t* status_dev, hipStream_t stream) {
+  MxRopeParams p{};
+  kvtc_status st = io_params(cfg, batch, layer, n_layers, const_cast<void*>(k), k_strides, const_cast<void*>(v),
+                             v_strides, pool, pool_bytes, cfg ? cfg->dtype : 0, status_dev, true, &p.io);
+  if (st != KVTC_OK) return st;
+  st = check_rope(rope, cfg->head_dim, &p);
+  if (st != KVTC_OK) return st;
+  if (misaligned(positions, 4) || (!positions && rope->axes != 1)) return KVTC_ERR_INVALID_ARG;
+  if (q_heads < 0 || (q_heads > 0 && n_layers != 1)) return KVTC_ERR_INVALID_ARG;
+  const int elem = cfg->dtype == KVTC_BF16 ? 2 : 4;
+  if (q_heads > 0) {
+    for (const int64_t s : {q_stride, q_out_stride})
+      if (s < 0 || s > ((int64_t)1 << 46) || (s * elem) % 16) return KVTC_ERR_INVALID_ARG;
+    if (batch->total_rows > 1 && q_out_stride < (int64_t)q_heads * cfg->head_dim) return KVTC_ERR_INVALID_ARG;
+  }
+  if (nothing_to_do(*batch)) return KVTC_OK;
+  if (q_heads > 0 && (!q || !q_out || misaligned(q) || misaligned(q_out) || (q == q_out && q_stride != q_out_stride)))
+    return KVTC_ERR_INVALID_ARG;
+  const int64_t all = (int64_t)2 * n_layers * cfg->kv_heads + q_heads;
+  p.positions = positions;
+  p.Hq = q_heads;
+  p.all = (int32_t)all;
+  p.slice = 16;
+  p.q = q;
+  p.q_out = q_out;
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  // (queries of rows before the first token too, so max_len is no bound here)
+  const int64_t units = std::max<int64_t>((std::min(batch->max_rows, batch->total_rows) + 2 * KVTC_MX_PAGE - 2) / KVTC_MX_PAGE, 1);
+  if (units * batch->n_seqs > kMaxGrid || all > 0x7FFFFFFF || (all + p.slice - 1) / p.slice > 65535) return KVTC_ERR_UNSUPPORTED;
+  p.io.n_units = (int32_t)units;
+  return launch_mx_rope(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, cfg->dtype == KVTC_FP32, stream) == hipSuccess
+             ? KVTC_OK
+             : KVTC_ERR_HIP;
+}
+
+kvtc_status kvtc_mx_tree(const kvtc_mx_batch* batch, const int32_t* parents, uint32_t* masks, int32_t words,
+                         int32_t* positions, uint32_t* status_dev, hipStream_t stream) {
+  kvtc_status st = check_batch(batch);
+  if (st == KVTC_OK) st = check_masks(*batch, masks, words);
+  if (st != KVTC_OK) return st;
+  if (misaligned(parents, 4) || misaligned(positions, 4) || misaligned(status_dev, 4)) return KVTC_ERR_INVALID_ARG;
+  if (nothing_to_do(*batch)) return KVTC_OK;
+  if (!parents) return KVTC_ERR_INVALID_ARG;
+  if (batch->n_seqs > kMaxGrid) return KVTC_ERR_UNSUPPORTED;
+  return launch_mx_tree(*batch, parents, masks, words, positions, status_dev, stream) == hipSuccess ? KVTC_OK
+                                                                                                  : KVTC_ERR_HIP;
+}
+
+kvtc_status kvtc_mx_attn_tree_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t q_heads,
+                                        int32_t shared_pages, size_t* ws_bytes) {
+  return kvtc_mx_attn_workspace(cfg, batch, q_heads, shared_pages, ws_bytes);
+}
+
+kvtc_status kvtc_mx_attn_tree(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,
+                              size_t pool_bytes, int32_t shared_pages, const uint32_t* masks, int32_t words,
+                              const void* q, int64_t q_stride, int32_t q_heads, float scale, void* out, float* lse,
+                              void* ws, size_t ws_bytes, uint32_t* status_dev, hipStream_t stream) {
+  kvtc_status st = check_config(cfg);
+  if (st == KVTC_OK) st = check_batch(batch);
+  if (st == KVTC_OK) st = check_masks(*batch, masks, words);
+  if (st != KVTC_OK) return st;
+  return attn_call(cfg, batch, layer, pool, pool_bytes, shared_pages, masks, words, q, q_stride, q_heads, scale, 0, out,
+                   lse, ws, ws_bytes, status_dev, stream);
+}
+
+kvtc_status kvtc_mx_keep(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
+                         const uint32_t* masks, int32_t words, const int32_t* nodes, void* pool, size_t pool_bytes,
+                         int32_t* lens_out, uint32_t* status_dev, hipStream_t stream) {
+  uint8_t* first;
+  kvtc_status st = check_call(cfg, batch, layer, n_layers, pool, pool_bytes, status_dev, &first);
+  if (st == KVTC_OK) st = check_masks(*batch, masks, words);
+  if (st != KVTC_OK) return st;
+  if (misaligned(nodes, 4) || misaligned(lens_out, 4)) return KVTC_ERR_INVALID_ARG;
+  if (batch->n_seqs == 0) return KVTC_OK;
+  if (!nodes || !lens_out || lens_out == batch->kv_lens) return KVTC_ERR_INVALID_ARG;
+  if (batch->n_seqs > kMaxGrid) return KVTC_ERR_UNSUPPORTED;
+  MxKeepParams p{};
+  p.b = *batch;
+  p.H = cfg->kv_heads;
+  p.n_layers = n_layers;
+  p.pool_pages = cfg->pool_pages;
+  p.words = words;
+  p.pool = first;
+  p.layer_bytes = layer_bytes(*cfg);
+  p.masks = masks;
+  p.nodes = nodes;
+  p.lens_out = lens_out;
+  p.status = status_dev;
+  return launch_mx_keep(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, stream) == hipSuccess ? KVTC_OK : KVTC_ERR_HIP;
 }
 
 }  // extern "C"

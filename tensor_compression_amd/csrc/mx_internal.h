@@ -53,6 +53,8 @@ struct MxAttnParams {
   float* ws_o;     // [slot][total_rows q_heads][D]
   float2* ws_ml;   // [slot][total_rows q_heads]: running maximum (base 2), sum
   uint32_t* status;
+  const uint32_t* masks;  // drafts: [total_rows][words], else null
+  int32_t words;
 };
 
 // Joining the partials: slots [0, prefix_splits) cover the prefix in chunks
@@ -73,7 +75,39 @@ hipError_t launch_mx_read(const MxIoParams& p, int D, int bk, int bv, bool f32, 
 // The passes of a call (either may be null), both before the join.
 hipError_t launch_mx_attn(const MxAttnParams* prefix, const MxAttnParams* own, int D, int bk, int bv, bool f32,
                           hipStream_t s);
+hipError_t launch_mx_attn_tree(const MxAttnParams* prefix, const MxAttnParams* own, int D, int bk, int bv, bool f32,
+                               hipStream_t s);
 hipError_t launch_mx_join(const MxJoinParams& p, bool f32, hipStream_t s);
+
+// Rotated rows: MxIoParams of the keys and values, and the queries beside them.
+struct MxRopeParams {
+  MxIoParams io;
+  const double* freqs;
+  const int32_t* positions;  // [axes][total_rows], or null: positions in the cache
+  uint64_t axis[2];          // axis of pair j: bits 2 (j % 32) of word j / 32
+  int32_t rot, interleaved;
+  int32_t Hq, all, slice;  // query heads; row vectors of a token: keys and values of every layer and head, queries; of a workgroup
+  const void* q;
+  void* q_out;
+  int64_t q_stride, q_out_stride;
+};
+hipError_t launch_mx_rope(const MxRopeParams& p, int D, int bk, int bv, bool f32, hipStream_t s);
+
+hipError_t launch_mx_tree(const kvtc_mx_batch& b, const int32_t* parents, uint32_t* masks, int words,
+                          int32_t* positions, uint32_t* status, hipStream_t s);
+
+// Moving the accepted rows' tokens.
+struct MxKeepParams {
+  kvtc_mx_batch b;
+  int32_t H, n_layers, pool_pages, words;
+  uint8_t* pool;  // record of (first layer, page 0, head 0)
+  int64_t layer_bytes;
+  const uint32_t* masks;
+  const int32_t* nodes;
+  int32_t* lens_out;
+  uint32_t* status;
+};
+hipError_t launch_mx_keep(const MxKeepParams& p, int D, int bk, int bv, hipStream_t s);
 
 #if defined(__HIPCC__)
 

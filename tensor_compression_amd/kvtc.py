@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libkvtc.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CAPACITY, ERR_CORRUPT, ERR_NONFINITE, ERR_HIP = range(7)
 FP32, BF16 = 0, 1
 PCA, WHT = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 SQ_BLOCK, SQ_KIVI = 1, 2
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CAPACITY", 4: "CORRUPT",
           5: "NONFINITE", 6: "HIP"}
@@ -64,6 +65,11 @@ class MxBatchStruct(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("total_rows", ctypes.c_int32),
                 ("max_rows", ctypes.c_int32), ("max_len", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("row_start", ctypes.c_void_p)]
+
+
+class MxRopeStruct(ctypes.Structure):
+    _fields_ = [("style", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("freqs", ctypes.c_void_p), ("axis", ctypes.c_char_p)]
 
 
 def make_pq_config(pq: dict) -> PqConfig:
@@ -174,6 +180,23 @@ EXPORTS = {
                                            ctypes.c_int32, ctypes.c_float, ctypes.c_int32, ctypes.c_void_p,
                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                            ctypes.c_void_p]),
+    "kvtc_mx_write_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvtc_mx_tree": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvtc_mx_attn_tree_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                                   ctypes.POINTER(ctypes.c_size_t)]),
+    "kvtc_mx_attn_tree": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                         ctypes.c_size_t, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "kvtc_mx_keep": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                    ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
 }
 
 _lib = None
@@ -576,6 +599,30 @@ class MxBatch:
         self.ref = ctypes.byref(self._c)
 
 
+class MxRope:
+    """A rotation by position (kvtc_mx_rope): freqs float64 [pairs] on the
+    cache's device (kept alive here; radians a unit of position, see
+    rope_freqs), the pairing style, and the axis of each pair (a sequence of
+    whole numbers below 4; None: one axis)."""
+
+    def __init__(self, freqs: torch.Tensor, style: int = ROPE_HALF, axis=None):
+        if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous() or not freqs.is_cuda:
+            raise ValueError("freqs is a contiguous float64 tensor [pairs] on a GPU")
+        axis = None if axis is None else [int(a) for a in axis]
+        if axis is not None and (len(axis) != freqs.numel() or any(not 0 <= a < 4 for a in axis)):
+            raise ValueError("axis gives each pair one of up to four axes")
+        self.freqs, self.axes = freqs, max(axis, default=0) + 1 if axis else 1
+        self.index = freqs.get_device()
+        self._axis = None if axis is None else bytes(axis)
+        self._c = MxRopeStruct(style, 2 * freqs.numel(), self.axes, 0, freqs.data_ptr(), self._axis)
+        self.ref = ctypes.byref(self._c)
+
+
+def rope_freqs(rot_dim: int, theta: float, device="cuda") -> torch.Tensor:
+    """theta^(-2j / rot_dim) for the pairs j of rot_dim rotated channels."""
+    return torch.tensor([theta ** (-2.0 * j / rot_dim) for j in range(rot_dim // 2)], dtype=torch.float64, device=device)
+
+
 class MxCache:
     """A microscaled paged cache: configuration and pool (uint8 [layers,
     pool_pages, kv_heads, record bytes], allocated here unless given).
@@ -686,28 +733,129 @@ class MxCache:
                    ks, vp, vs, BF16 if k_out.dtype == torch.bfloat16 else FP32, self._status(status))
         return k_out, v_out
 
+    def write_rope(self, batch: MxBatch, k: torch.Tensor, v: torch.Tensor, rope: MxRope,
+                   positions: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, layer: int = 0, status: torch.Tensor | None = None, stream=None):
+        """kvtc_mx_write_rope: as write, the keys rotated on the way; positions
+        int32 [axes, total_rows] ([total_rows] for one axis; default: the rows'
+        positions in the cache).  q [total_rows, q_heads, head_dim], rotated
+        into out, which may be q and is allocated on the call's stream when not
+        given; returns out (None without q)."""
+        index = self._index
+        if k.dtype != self.dtype or v.dtype != self.dtype:
+            raise ValueError(f"keys and values are {self.dtype}")
+        if rope.index != index:
+            raise ValueError("a rotation on another device than the cache")
+        n = k.shape[0] if k.dim() == 4 else 1
+        (kp, ks), (vp, vs) = self._rows(k, batch, n), self._rows(v, batch, n)
+        pp = None
+        if positions is not None:
+            sh = positions.shape
+            if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.get_device() != index or \
+                    not (sh == (rope.axes, batch.total_rows) or (rope.axes == 1 and sh == (batch.total_rows,))):
+                raise ValueError(f"positions are a contiguous int32 tensor [{rope.axes}, total_rows]")
+            pp = positions.data_ptr()
+        heads, qs, os, qp, op = 0, 0, 0, None, None
+        if q is not None:
+            sh, qst = self._queries(q, batch)
+            if out is None:
+                with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+                    out = torch.empty(sh, dtype=q.dtype, device=self.device)
+            if out is not q:
+                if out.shape != sh:
+                    raise ValueError("out is a tensor of the queries' shape")
+                ost = self._queries(out, batch)[1]
+            else:
+                ost = qst
+            heads, qs, os, qp, op = sh[1], qst, ost, q.data_ptr(), out.data_ptr()
+        elif out is not None:
+            raise ValueError("out without queries")
+        self._call(self._lib.kvtc_mx_write_rope, stream, self._ref, batch.ref, layer, n, rope.ref, pp, kp, ks, vp, vs,
+                   qp, qs, heads, op, os, self._pool_ptr, self.pool_bytes, self._status(status))
+        return out
+
+    def _masks(self, masks, batch):
+        if masks.dtype != torch.int32 or masks.dim() != 2 or masks.shape[0] != batch.total_rows or \
+                not masks.is_contiguous() or masks.get_device() != self._index:
+            raise ValueError("masks are a contiguous int32 tensor [total_rows, words]")
+        return masks.data_ptr(), masks.shape[1]
+
+    def _ints(self, t, n, what):
+        if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != self._index:
+            raise ValueError(f"{what}: a contiguous int32 tensor [{n}] on the cache's device")
+        return t.data_ptr()
+
+    def tree(self, batch: MxBatch, parents: torch.Tensor, masks: torch.Tensor | None = None,
+             positions: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+        """kvtc_mx_tree: parents int32 [total_rows] -> (masks int32 [total_rows,
+        words], positions int32 [total_rows]), allocated on the call's stream
+        when not given."""
+        if batch.index != self._index:
+            raise ValueError("a batch on another device than the cache")
+        pp = self._ints(parents, batch.total_rows, "parents")
+        if masks is None or positions is None:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+                if masks is None:
+                    masks = torch.empty(batch.total_rows, max(-(-batch.max_rows // 32), 1), dtype=torch.int32, device=self.device)
+                if positions is None:
+                    positions = torch.empty(batch.total_rows, dtype=torch.int32, device=self.device)
+        mp, words = self._masks(masks, batch)
+        op = self._ints(positions, batch.total_rows, "positions")
+        self._call(self._lib.kvtc_mx_tree, stream, batch.ref, pp, mp, words, op, self._status(status))
+        return masks, positions
+
+    def keep(self, batch: MxBatch, nodes: torch.Tensor, masks: torch.Tensor, layer: int = 0, layers: int | None = None,
+             lens_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """kvtc_mx_keep on `layers` layers from `layer` on (default: all that
+        follow): nodes int32 [n_seqs] -> the lengths after it, int32 [n_seqs],
+        allocated on the call's stream when not given."""
+        if batch.index != self._index:
+            raise ValueError("a batch on another device than the cache")
+        n = batch.kv_lens.numel()
+        mp, words = self._masks(masks, batch)
+        np_ = self._ints(nodes, n, "nodes")
+        if lens_out is None:
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+                lens_out = torch.empty(n, dtype=torch.int32, device=self.device)
+        self._call(self._lib.kvtc_mx_keep, stream, self._ref, batch.ref, layer,
+                   self.cfg["layers"] - layer if layers is None else layers, mp, words, np_, self._pool_ptr,
+                   self.pool_bytes, self._ints(lens_out, n, "lens_out"), self._status(status))
+        return lens_out
+
     def workspace(self, batch: MxBatch, q_heads: int, shared_pages: int = 0) -> torch.Tensor:
         """A workspace for the attention of this batch's bounds."""
+        return self._workspace(self._lib.kvtc_mx_attn_workspace, batch, q_heads, shared_pages)
+
+    def workspace_tree(self, batch: MxBatch, q_heads: int, shared_pages: int = 0) -> torch.Tensor:
+        """A workspace for attention_tree."""
+        return self._workspace(self._lib.kvtc_mx_attn_tree_workspace, batch, q_heads, shared_pages)
+
+    def _workspace(self, fn, batch, q_heads, shared_pages):
         n = ctypes.c_size_t(0)
-        _check(lib().kvtc_mx_attn_workspace(self._ref, batch.ref, q_heads, shared_pages, ctypes.byref(n)),
-               "kvtc_mx_attn_workspace")
+        _check(fn(self._ref, batch.ref, q_heads, shared_pages, ctypes.byref(n)), fn.__name__)
         return torch.empty(max(n.value, 16), dtype=torch.uint8, device=self.device)
 
-    def _attention(self, batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream):
+    def _queries(self, q, batch):
+        """(shape, row stride) of queries [total_rows, heads, head_dim]."""
         self._own(q)
         if batch.index != self._index:
             raise ValueError("a batch on another device than the cache")
-        sh, st, D, index = q.shape, q.stride(), self._head[1], self._index
+        sh, st, D = q.shape, q.stride(), self._head[1]
         if q.dtype != self.dtype or len(sh) != 3 or sh[0] != batch.total_rows or sh[2] != D or st[2] != 1 or \
                 (st[1] != D and sh[1] > 1):
             raise ValueError(f"queries are {self.dtype} [total_rows, heads, {D}] with contiguous heads")
+        return sh, st[0] if sh[0] > 1 else 0
+
+    def _attention(self, batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream, masks=None):
+        (sh, q_stride), D, index = self._queries(q, batch), self._head[1], self._index
         heads = sh[1]
         if out is None or ws is None:
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 if out is None:
                     out = torch.empty(sh, dtype=q.dtype, device=self.device)
                 if ws is None:
-                    ws = self.workspace(batch, heads, shared_pages or 0)
+                    make = self.workspace if masks is None else self.workspace_tree
+                    ws = make(batch, heads, shared_pages or 0)
         if out.dtype != q.dtype or out.shape != sh or not out.is_contiguous() or out.get_device() != index:
             raise ValueError("out is a contiguous tensor of the queries' type and shape")
         lp = None
@@ -718,8 +866,13 @@ class MxCache:
             lp = lse.data_ptr()
         if ws.get_device() != index or not ws.is_contiguous():
             raise ValueError("the workspace is a contiguous tensor on the cache's device")
-        tail = (q.data_ptr(), st[0] if sh[0] > 1 else 0, heads, scale if scale is not None else D ** -0.5,
-                1 if causal else 0, out.data_ptr(), lp, ws.data_ptr(), ws.nbytes, self._status(status))
+        head = (q.data_ptr(), q_stride, heads, scale if scale is not None else D ** -0.5)
+        tail = (out.data_ptr(), lp, ws.data_ptr(), ws.nbytes, self._status(status))
+        if masks is not None:
+            self._call(self._lib.kvtc_mx_attn_tree, stream, self._ref, batch.ref, layer, self._pool_ptr,
+                       self.pool_bytes, shared_pages, *self._masks(masks, batch), *head, *tail)
+            return (out, lse) if lse is not None else out
+        tail = (*head, 1 if causal else 0, *tail)
         if shared_pages is None:
             self._call(self._lib.kvtc_mx_attn, stream, self._ref, batch.ref, layer, self._pool_ptr, self.pool_bytes,
                        *tail)
@@ -743,6 +896,15 @@ class MxCache:
         """kvtc_mx_attn_shared: as attention, for sequences whose first
         shared_pages pages are the first sequence's."""
         return self._attention(batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream)
+
+    def attention_tree(self, batch: MxBatch, q: torch.Tensor, masks: torch.Tensor, shared_pages: int = 0,
+                       scale: float | None = None, layer: int = 0, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                       status: torch.Tensor | None = None, stream=None):
+        """kvtc_mx_attn_tree: as attention, for drafts: each row attends to the
+        tokens before the draft and to the rows that its mask (int32
+        [total_rows, words], see tree) names.  ws: from workspace_tree."""
+        return self._attention(batch, q, shared_pages, scale, False, layer, out, lse, ws, status, stream, masks)
 
 
 def freq_tables(counts: torch.Tensor, alphabet: torch.Tensor, scale_bits: int):

@@ -141,3 +141,70 @@ def attention(kp, vp, table, lens, starts, q, scale, causal):
                     mass[r, h] = p @ np.abs(vv)
                     spread[r, h] = (scale * (np.abs(kk) @ np.abs(q[r, h]))).max()
     return out, lse, mass, spread
+
+
+# ---- rotation, drafts
+
+
+def rotate(x, pos, freqs, axis, half):
+    """x [..., rows, heads, D] float64, pos [axes][rows] -> rotated: the pairs
+    of the first 2 len(freqs) channels by pos[axis[j]] freqs[j]."""
+    x = np.array(x, np.float64)
+    p = len(freqs)
+    with np.errstate(invalid="ignore", over="ignore"):
+        for j in range(p):
+            a, b = (j, j + p) if half else (2 * j, 2 * j + 1)
+            ang = np.asarray(pos[axis[j]], np.float64) * freqs[j]
+            c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+            u, v = x[..., a].copy(), x[..., b].copy()
+            x[..., a], x[..., b] = u * c - v * s, u * s + v * c
+    return x
+
+
+def tree(parents):
+    """Sorted rows that each row of a draft sees: itself and its ancestors."""
+    seen = []
+    for i, p in enumerate(parents):
+        seen.append((seen[p] if p >= 0 else []) + [i])
+    return seen
+
+
+def mask_words(seen, words):
+    """Rows seen -> int32 words [rows][words]."""
+    out = np.zeros((len(seen), words), np.uint32)
+    for i, rows in enumerate(seen):
+        for j in rows:
+            out[i, j // 32] |= np.uint32(1 << (j % 32))
+    return out.view(np.int32)
+
+
+def attention_seen(kp, vp, table, lens, starts, q, scale, seen):
+    """attention() of rows that see the tokens before their sequence's rows and
+    the rows seen[z][i] of it."""
+    rows, Hq, D = q.shape
+    G = Hq // kp.shape[1]
+    out, lse = np.zeros((rows, Hq, D)), np.full((rows, Hq), -np.inf)
+    mass, spread = np.zeros((rows, Hq, D)), np.zeros((rows, Hq))
+    with np.errstate(invalid="ignore"):
+        for z, ln in enumerate(lens):
+            n = starts[z + 1] - starts[z]
+            if n == 0 or ln == 0:
+                continue
+            k, v = tokens(kp, vp, table[z][: -(-ln // PAGE)], ln)
+            base = ln - n
+            for i in range(n):
+                at = list(range(max(base, 0))) + [base + j for j in seen[z][i] if base + j >= 0]
+                if not at:
+                    continue
+                r = starts[z] + i
+                for h in range(Hq):
+                    kk, vv = k[h // G, at], v[h // G, at]
+                    s = scale * (kk @ q[r, h])
+                    m = s.max()
+                    p = np.exp(s - m)
+                    lse[r, h] = m + np.log(p.sum())
+                    p /= p.sum()
+                    out[r, h] = p @ vv
+                    mass[r, h] = p @ np.abs(vv)
+                    spread[r, h] = (scale * (np.abs(kk) @ np.abs(q[r, h]))).max()
+    return out, lse, mass, spread

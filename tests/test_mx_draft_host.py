@@ -1,0 +1,190 @@
+"""Rotated appends and drafts on the microscaled cache, on the CPU: the plain
+implementation's own pins, and what the library and the binding refuse before
+anything is launched."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mx_ref
+from tensor_compression_amd import kvtc
+from test_mx_host import CAP, INV, P, UNS, batch, cfg, size, strides
+
+CALLS = ("rope", "attn", "keep")
+
+
+def rope(axis=None, **kw):
+    r = dict(style=0, rot_dim=128, axes=1, reserved=0, freqs=P, axis=axis)
+    r.update(kw)
+    return kvtc.MxRopeStruct(*[r[f] for f, _ in kvtc.MxRopeStruct._fields_])
+
+
+def call(name, c=None, b=None, r=None, **kw):
+    c, b, r = c or cfg(), b or batch(), r or rope()
+    a = dict(layer=0, n_layers=1, positions=P, k=P, ks=strides(0, 128, 512), v=P, vs=strides(0, 128, 512), q=P, q_stride=1024,
+             q_heads=8, q_out=P + 4096, q_out_stride=1024, pool=P, pool_bytes=1 << 40, status=P, masks=P, words=1, shared=2,
+             scale=0.1, out=P, lse=P, ws=P, ws_bytes=1 << 40, nodes=P, lens_out=P + 64, parents=P, tree_positions=P)
+    a.update(kw)
+    L, cr, br = kvtc.lib(), ctypes.byref(c), ctypes.byref(b)
+    if name == "rope":
+        return L.kvtc_mx_write_rope(cr, br, a["layer"], a["n_layers"], ctypes.byref(r), a["positions"], a["k"], a["ks"],
+                                    a["v"], a["vs"], a["q"], a["q_stride"], a["q_heads"], a["q_out"], a["q_out_stride"],
+                                    a["pool"], a["pool_bytes"], a["status"], None)
+    if name == "tree":
+        return L.kvtc_mx_tree(br, a["parents"], a["masks"], a["words"], a["tree_positions"], a["status"], None)
+    if name == "keep":
+        return L.kvtc_mx_keep(cr, br, a["layer"], a["n_layers"], a["masks"], a["words"], a["nodes"], a["pool"],
+                              a["pool_bytes"], a["lens_out"], a["status"], None)
+    return L.kvtc_mx_attn_tree(cr, br, a["layer"], a["pool"], a["pool_bytes"], a["shared"], a["masks"], a["words"], a["q"],
+                               a["q_stride"], a["q_heads"], a["scale"], a["out"], a["lse"], a["ws"], a["ws_bytes"],
+                               a["status"], None)
+
+
+# ---- the plain implementation
+
+
+@pytest.mark.parametrize("half", [True, False])
+def test_rotation_keeps_lengths_and_adds_up(half):
+    """A pair's length stays; turning by t and then u is turning by t + u; the
+    product of two rotated vectors depends on the distance alone."""
+    rng = np.random.default_rng(0)
+    f, axis = [10000.0 ** (-j / 32) for j in range(32)], [j % 2 for j in range(32)]
+    x, y = rng.standard_normal((2, 5, 3, 80))
+    t, u = rng.integers(-1000, 1000, (2, 2, 5))
+    a = mx_ref.rotate(x, t, f, axis, half)
+    assert np.allclose(np.square(a).sum(-1), np.square(x).sum(-1), rtol=1e-12) and np.array_equal(a[..., 64:], x[..., 64:])
+    assert np.allclose(mx_ref.rotate(a, u, f, axis, half), mx_ref.rotate(x, t + u, f, axis, half), atol=1e-10)
+    b = mx_ref.rotate(y, t + 77, f, axis, half)
+    want = (x * mx_ref.rotate(y, np.full((2, 5), 77), f, axis, half)).sum(-1)
+    assert np.allclose((a * b).sum(-1), want, atol=1e-10)
+    # the first pair by a radian
+    one = mx_ref.rotate(np.eye(80)[:1, None], np.ones((2, 1), int), f, axis, half)[0, 0]
+    assert np.isclose(one[0], np.cos(1)) and np.isclose(one[32 if half else 1], np.sin(1))
+
+
+def test_tree_and_masks():
+    seen = mx_ref.tree([-1, 0, 0, 2, -1, 4, 3])
+    assert seen == [[0], [0, 1], [0, 2], [0, 2, 3], [4], [4, 5], [0, 2, 3, 6]]
+    assert mx_ref.mask_words(seen, 2).tolist() == [[1, 0], [3, 0], [5, 0], [13, 0], [16, 0], [48, 0], [77, 0]]
+    assert mx_ref.mask_words([[31, 32]], 2).tolist() == [[-2 ** 31, 1]]
+
+
+def test_attention_of_a_chain_is_causal():
+    rng = np.random.default_rng(1)
+    D, bk, bv = 64, 8, 8
+    pool = np.zeros((4, 2, mx_ref.record_bytes(D, bk, bv)), np.uint8)
+    lens, starts, table = [20, 33], [0, 20, 25], [[0], [1, 3, 2]]
+    table[0] = [0, 0]
+    k, v = rng.standard_normal((2, 33, 2, D))
+    mx_ref.write(pool, table[1:], [33], [0, 33], k, v, D, bk, bv)
+    kp, vp = mx_ref.unpack(pool, D, bk, bv)
+    q = rng.standard_normal((25, 4, D))
+    seen = [mx_ref.tree(list(range(-1, n - 1))) for n in (20, 5)]
+    for a, b in zip(mx_ref.attention_seen(kp, vp, table, lens, starts, q, 0.1, seen),
+                    mx_ref.attention(kp, vp, table, lens, starts, q, 0.1, True)):
+        # sums of at most 64 terms below 10, whose order may differ: 64 steps of 2^-53 of 640
+        assert np.array_equal(np.isinf(a), np.isinf(b)) and np.allclose(a, b, rtol=0, atol=64 * 2.0 ** -53 * 640)
+
+
+# ---- refusals
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(layers=0), INV), (dict(kv_heads=0), INV), (dict(pool_pages=0), INV), (dict(dtype=2), INV),
+    (dict(bits_k=5), INV), (dict(bits_v=16), INV), (dict(head_dim=96), UNS), (dict(layers=8193, kv_heads=8), UNS)])
+def test_bad_configurations(bad, want):
+    for name in CALLS:
+        assert call(name, c=cfg(**bad)) == want, name
+    n = ctypes.c_size_t(0)
+    assert kvtc.lib().kvtc_mx_attn_tree_workspace(ctypes.byref(cfg(**bad)), ctypes.byref(batch()), 8, 0, ctypes.byref(n)) == want
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_seqs=-1), dict(max_pages=0), dict(total_rows=-1), dict(max_rows=-1), dict(max_len=-1), dict(max_len=97),
+    dict(reserved=1), dict(page_table=None), dict(kv_lens=None), dict(row_start=None), dict(page_table=P + 2),
+    dict(kv_lens=P + 1), dict(row_start=P + 2)])
+def test_bad_batches(bad):
+    for name in CALLS + ("tree",):
+        assert call(name, b=batch(**bad)) == INV, name
+    n = ctypes.c_size_t(0)
+    assert kvtc.lib().kvtc_mx_attn_tree_workspace(ctypes.byref(cfg()), ctypes.byref(batch(**bad)), 8, 0, ctypes.byref(n)) == INV
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_bad_pool_layer_status(name):
+    need = size(cfg())[2]
+    for bad, want in ((dict(pool=None), INV), (dict(pool=P + 8), INV), (dict(pool_bytes=need - 1), CAP),
+                      (dict(layer=-1), INV), (dict(layer=2), INV), (dict(status=P + 2), INV)):
+        assert call(name, **bad) == want, bad
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(style=2), INV), (dict(rot_dim=0), INV), (dict(rot_dim=144), INV), (dict(rot_dim=-16), INV), (dict(rot_dim=24), UNS),
+    (dict(rot_dim=127), UNS), (dict(axes=0), INV), (dict(axes=5), INV), (dict(reserved=1), INV), (dict(freqs=None), INV),
+    (dict(freqs=P + 4), INV), (dict(axis=bytes([0] * 63 + [1])), INV), (dict(axes=3, axis=bytes([3] + [0] * 63)), INV)])
+def test_bad_rotations(bad, want):
+    assert call("rope", r=rope(**bad)) == want
+    assert call("rope", r=rope(**bad), q_heads=0, q=None, q_out=None) == want
+
+
+def test_bad_rotated_rows():
+    for bad in (dict(k=None), dict(v=None), dict(k=P + 8), dict(v=P + 2), dict(ks=None), dict(vs=None),
+                dict(ks=strides(0, 128, -512)), dict(vs=strides(0, 124, 512)), dict(ks=strides(0, 128, 2 ** 47)),
+                dict(n_layers=0), dict(n_layers=3), dict(layer=1, n_layers=2), dict(positions=P + 2), dict(q=None),
+                dict(q_out=None), dict(q=P + 8), dict(q_out=P + 4), dict(q_heads=-1), dict(q_stride=-8), dict(q_stride=12),
+                dict(q_out_stride=12), dict(q_out_stride=1016), dict(q_out_stride=2 ** 47), dict(n_layers=2),
+                dict(q_out=P, q_stride=2048)):
+        assert call("rope", **bad) == INV, bad
+    assert call("rope", r=rope(axes=2, axis=bytes([0, 1] * 32)), positions=None) == INV
+    assert call("rope", b=batch(n_seqs=2 ** 20, total_rows=2 ** 20, max_rows=2 ** 10)) == UNS
+    assert call("rope", c=cfg(layers=16384), n_layers=1, q_heads=2 ** 30 // 128, q_stride=2 ** 30, q_out_stride=2 ** 30) == UNS
+
+
+@pytest.mark.parametrize("name", ["attn", "keep", "tree"])
+def test_bad_masks(name):
+    for bad, want in ((dict(masks=None), INV), (dict(masks=P + 2), INV), (dict(words=0), INV), (dict(words=-1), INV),
+                      (dict(words=129), UNS)):
+        assert call(name, **bad) == want, bad
+    assert call(name, b=batch(max_rows=33)) == INV
+    assert call(name, b=batch(max_rows=4097, total_rows=4097), words=129) == UNS
+
+
+def test_bad_trees_and_nodes():
+    for bad in (dict(parents=None), dict(parents=P + 2), dict(tree_positions=P + 2), dict(status=P + 1)):
+        assert call("tree", **bad) == INV, bad
+    for bad in (dict(nodes=None), dict(nodes=P + 2), dict(lens_out=None), dict(lens_out=P + 2), dict(lens_out=P),
+                dict(n_layers=0), dict(n_layers=3), dict(layer=1, n_layers=2)):
+        assert call("keep", **bad) == INV, bad
+    for name in ("tree", "keep"):
+        assert call(name, b=batch(n_seqs=2 ** 24)) == UNS
+
+
+def test_bad_tree_attention():
+    for bad in (dict(q=None), dict(out=None), dict(q=P + 2), dict(out=P + 8), dict(lse=P + 2), dict(ws=P + 8),
+                dict(q_stride=-8), dict(q_stride=12), dict(q_heads=0), dict(q_heads=6), dict(scale=0.0), dict(scale=-1.0),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=2.0 ** 101), dict(shared=-1), dict(shared=7)):
+        assert call("attn", **bad) == INV, bad
+    assert call("attn", b=batch(total_rows=2 ** 28)) == UNS
+    n = ctypes.c_size_t(0)
+    assert kvtc.lib().kvtc_mx_attn_tree_workspace(ctypes.byref(cfg()), ctypes.byref(batch()), 8, 2, ctypes.byref(n)) == kvtc.OK
+    assert n.value > 0
+    assert call("attn", ws_bytes=n.value - 1) == CAP and call("attn", ws=None) == INV
+    assert kvtc.lib().kvtc_mx_attn_tree_workspace(ctypes.byref(cfg()), ctypes.byref(batch()), 8, 2, None) == INV
+
+
+@pytest.mark.parametrize("name", ("rope", "attn", "tree"))
+def test_nothing_to_do(name):
+    for b in (batch(n_seqs=0, page_table=None, kv_lens=None, row_start=None), batch(total_rows=0), batch(max_rows=0)):
+        assert call(name, b=b, k=None, v=None, q=None, q_out=None, out=None, ws=None, ws_bytes=0, masks=None, parents=None) == kvtc.OK
+    assert call("keep", b=batch(n_seqs=0, page_table=None, kv_lens=None, row_start=None), masks=None, nodes=None, lens_out=None) == kvtc.OK
+
+
+def test_rotations_of_the_binding():
+    """Frequencies that the kernels could not read, axes past four."""
+    f = kvtc.rope_freqs(64, 1e4, device="cpu")
+    assert f.dtype == torch.float64 and f[0] == 1 and np.isclose(f[16].item(), 1e-2) and f.numel() == 32
+    with pytest.raises(ValueError):
+        kvtc.MxRope(f)
+    with pytest.raises(ValueError):
+        kvtc.MxRope(f.float())
