@@ -701,8 +701,8 @@ typedef struct kvtc_mx_rope {
  * between: their codes are those of the exact rotation, but where that comes
  * within 2^-51 (|a| + |b|) of a rounding border.  Rotated keys past the end of
  * fp32 saturate.  Values are quantised as kvtc_mx_write does.  Queries are rotated
- * in fp32 (cos and sin rounded to it from fp64) and rounded once to their
- * type: element (r, h, c) from q + r q_stride + h head_dim + c to q_out +
+ * in fp32 (by cos and sin of the fp64 angle within 2.3 2^-24) and rounded once
+ * to their type: element (r, h, c) from q + r q_stride + h head_dim + c to q_out +
  * r q_out_stride + h head_dim + c.  q_out may be q with the same stride; it
  * must not overlap the call's inputs otherwise.  q_heads 0: no queries, q and
  * q_out are not looked at; else n_layers must be 1.  q_stride and

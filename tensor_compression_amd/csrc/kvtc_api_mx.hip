@@ -397,18 +397,18 @@ kvtc_status kvtc_mx_write_rope(const kvtc_mx_config* cfg, const kvtc_mx_batch* b
   if (nothing_to_do(*batch)) return KVTC_OK;
   if (q_heads > 0 && (!q || !q_out || misaligned(q) || misaligned(q_out) || (q == q_out && q_stride != q_out_stride)))
     return KVTC_ERR_INVALID_ARG;
-  const int64_t all = (int64_t)2 * n_layers * cfg->kv_heads + q_heads;
+  auto slices = [](int64_t n) { return (n + kMxRopeSlice - 1) / kMxRopeSlice; };
+  const int64_t parts = 2 * slices(cfg->kv_heads) + slices(q_heads);
   p.positions = positions;
   p.Hq = q_heads;
-  p.all = (int32_t)all;
-  p.slice = 16;
+  p.parts = (int32_t)parts;
   p.q = q;
   p.q_out = q_out;
   p.q_stride = q_stride;
   p.q_out_stride = q_out_stride;
   // (queries of rows before the first token too, so max_len is no bound here)
   const int64_t units = std::max<int64_t>((std::min(batch->max_rows, batch->total_rows) + 2 * KVTC_MX_PAGE - 2) / KVTC_MX_PAGE, 1);
-  if (units * batch->n_seqs > kMaxGrid || all > 0x7FFFFFFF || (all + p.slice - 1) / p.slice > 65535) return KVTC_ERR_UNSUPPORTED;
+  if (units * batch->n_seqs > kMaxGrid || parts * n_layers > 65535) return KVTC_ERR_UNSUPPORTED;
   p.io.n_units = (int32_t)units;
   return launch_mx_rope(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, cfg->dtype == KVTC_FP32, stream) == hipSuccess
              ? KVTC_OK

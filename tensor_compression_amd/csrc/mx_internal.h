@@ -79,6 +79,7 @@ hipError_t launch_mx_attn_tree(const MxAttnParams* prefix, const MxAttnParams* o
                                hipStream_t s);
 hipError_t launch_mx_join(const MxJoinParams& p, bool f32, hipStream_t s);
 
+constexpr int kMxRopeSlice = 8;  // row vectors of a workgroup
 // Rotated rows: MxIoParams of the keys and values, and the queries beside them.
 struct MxRopeParams {
   MxIoParams io;
@@ -86,7 +87,7 @@ struct MxRopeParams {
   const int32_t* positions;  // [axes][total_rows], or null: positions in the cache
   uint64_t axis[2];          // axis of pair j: bits 2 (j % 32) of word j / 32
   int32_t rot, interleaved;
-  int32_t Hq, all, slice;  // query heads; row vectors of a token: keys and values of every layer and head, queries; of a workgroup
+  int32_t Hq, parts;  // query heads; workgroups along a layer's row vectors (keys, values, queries, each kind by itself)
   const void* q;
   void* q_out;
   int64_t q_stride, q_out_stride;

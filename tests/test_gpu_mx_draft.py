@@ -30,8 +30,8 @@ def own_positions(c):
 
 
 def check_queries(q, got, pos, rot, half, axis, dtype, what, theta=1e4):
-    """cos and sin are rounded to fp32, their products and the sum once each:
-    2^-24 of |a| + |b| at most four times over, and the fp64 angle's own error
+    """cos and sin are within 2.3 2^-24, one product is rounded, then the sum:
+    at most 4 2^-24 of |a| + |b|, and the fp64 angle's own error
     (2^-53 of it, with a factor of 4); then half a step of the output."""
     want = mx_ref.rotate(np64(q), pos, freqs_of(rot, theta), axis, half)
     x = np.abs(np64(q))
