@@ -675,7 +675,8 @@ def test_offsets_past_32_bits():
 def test_captured_drafts_follow_the_device_arrays():
     """A whole step captured once (tree, rotated append, attention behind a
     prefix and without, keeping) and replayed while lengths, rows, trees and
-    nodes change; every replay against the eager calls."""
+    nodes change; every replay against the eager calls.  (At most one sequence
+    writes into the two shared pages: two would write the same rows.)"""
     D, H, G, n, most = 128, 2, 4, 3, 3000  # ranges, so workspaces
     c = Case(D, 8, 4, kvtc.BF16, H, [8] * n, [most] * n, seed=14, shared=2)
     c.fill()
@@ -707,7 +708,7 @@ def test_captured_drafts_follow_the_device_arrays():
     with torch.cuda.graph(g):
         step(bufs[0])
     for r, (ln, rows) in enumerate([((90, 40, 48), (8, 4, 8)), ((700, 128, 33), (12, 0, 12)), ((129, 640, 44), (3, 12, 9)),
-                                    ((5, 12, 0), (8, 12, 2)), ((257, 90, 40), (1, 1, 1))]):
+                                    ((5, 52, 0), (8, 12, 2)), ((257, 90, 40), (1, 1, 1))]):
         lens.copy_(dev(list(ln), torch.int32))
         at = [0] + [int(x) for x in np.cumsum(rows)]
         starts.copy_(dev(at, torch.int32))
