@@ -188,7 +188,8 @@ struct AttnPlan {
   int64_t slots, ws;
 };
 
-kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q_heads, int32_t shared, AttnPlan* a) {
+kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q_heads, int32_t shared, bool tree,
+                      AttnPlan* a) {
   if (q_heads < c.kv_heads || q_heads % c.kv_heads) return KVTC_ERR_INVALID_ARG;
   if (shared < 0 || shared > b.max_pages) return KVTC_ERR_INVALID_ARG;
   if ((int64_t)b.total_rows * q_heads > 0x7FFFFFFF) return KVTC_ERR_UNSUPPORTED;
@@ -218,6 +219,10 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
     // 8192: 140 -> 103).
     a->together = a->prefix.nt == 8 && a->own.nt == 1 && !a->once;
     if (a->together) a->own.waves = 4;
+    // Drafts: also where both take the kernel for many rows.
+    if (tree && a->prefix.nt == 8 && a->own.nt == 8 &&
+        (a->own.tiles * a->own.nsplit * b.n_seqs + a->prefix.tiles * a->prefix.nsplit) * c.kv_heads <= kMaxGrid)
+      a->together = true;
   }
   a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
@@ -239,7 +244,7 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   kvtc_status st = check_call(cfg, b, layer, 1, pool, pool_bytes, status, &first);
   if (st != KVTC_OK) return st;
   AttnPlan a;
-  st = plan_attn(*cfg, *b, q_heads, shared, &a);
+  st = plan_attn(*cfg, *b, q_heads, shared, masks != nullptr, &a);
   if (st != KVTC_OK) return st;
   const int elem = cfg->dtype == KVTC_BF16 ? 2 : 4;
   if (!(scale > 0.0f && scale <= 0x1p100f) || !isnormal(scale) || (causal != 0 && causal != 1)) return KVTC_ERR_INVALID_ARG;
@@ -295,6 +300,12 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   if (!a.prefix.nsplit && a.own.nt < 8 && a.own.tiles == 1 && a.own.nsplit == 1 && b->n_seqs > per_round &&
       b->n_seqs <= 256 && b->max_len >= 2048)
     p.pair = (int32_t)per_round;
+  // Drafts in two tiles of 32 rows, more workgroups than the card holds at once
+  // (two a unit): the longest sequences first (64 of 511 to 8191 tokens, 5 to
+  // 16 rows of 4 heads each: 141 -> 112 us).
+  if (masks && !a.prefix.nsplit && a.own.nt == 2 && a.own.tiles > 1 && a.own.nsplit == 1 &&
+      a.own.tiles * cfg->kv_heads * b->n_seqs > 512 && b->n_seqs <= 256 && b->max_len >= 2048)
+    p.pair = 1;
   p.once = a.once;
   p.together = a.together;
   const auto launch = masks ? launch_mx_attn_tree : launch_mx_attn;
@@ -318,6 +329,18 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
   j.lse = lse;
   j.status = status;
   return launch_mx_join(j, f32, stream) == hipSuccess ? KVTC_OK : KVTC_ERR_HIP;
+}
+
+kvtc_status attn_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t q_heads, int32_t shared_pages,
+                           bool tree, size_t* ws_bytes) {
+  kvtc_status st = check_config(cfg);
+  if (st == KVTC_OK) st = check_batch(batch);
+  if (st != KVTC_OK) return st;
+  if (!ws_bytes) return KVTC_ERR_INVALID_ARG;
+  AttnPlan a;
+  st = plan_attn(*cfg, *batch, q_heads, shared_pages, tree, &a);
+  if (st == KVTC_OK) *ws_bytes = (size_t)a.ws;
+  return st;
 }
 
 }  // namespace
@@ -349,14 +372,7 @@ kvtc_status kvtc_mx_read(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, 
 
 kvtc_status kvtc_mx_attn_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t q_heads,
                                    int32_t shared_pages, size_t* ws_bytes) {
-  kvtc_status st = check_config(cfg);
-  if (st == KVTC_OK) st = check_batch(batch);
-  if (st != KVTC_OK) return st;
-  if (!ws_bytes) return KVTC_ERR_INVALID_ARG;
-  AttnPlan a;
-  st = plan_attn(*cfg, *batch, q_heads, shared_pages, &a);
-  if (st == KVTC_OK) *ws_bytes = (size_t)a.ws;
-  return st;
+  return attn_workspace(cfg, batch, q_heads, shared_pages, false, ws_bytes);
 }
 
 kvtc_status kvtc_mx_attn(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,
@@ -430,7 +446,7 @@ kvtc_status kvtc_mx_tree(const kvtc_mx_batch* batch, const int32_t* parents, uin
 
 kvtc_status kvtc_mx_attn_tree_workspace(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t q_heads,
                                         int32_t shared_pages, size_t* ws_bytes) {
-  return kvtc_mx_attn_workspace(cfg, batch, q_heads, shared_pages, ws_bytes);
+  return attn_workspace(cfg, batch, q_heads, shared_pages, true, ws_bytes);
 }
 
 kvtc_status kvtc_mx_attn_tree(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, const void* pool,

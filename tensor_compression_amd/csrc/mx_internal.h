@@ -47,7 +47,7 @@ struct MxAttnParams {
   int32_t fold;      // pair long tiles with short ones
   int32_t once;      // read the codes past the caches (nt 1)
   int32_t together;  // (own tokens) in one launch with the prefix
-  int32_t pair;      // sequences by length, the longest `pair` in rising order, then falling; 0: as they come
+  int32_t pair;      // sequences by length, the longest `pair` in rising order, then falling; 0: as they come (waves 4)
   int32_t tiles, nsplit, chunk;
   int32_t slot0;   // first partial slot of this pass
   float* ws_o;     // [slot][total_rows q_heads][D]
