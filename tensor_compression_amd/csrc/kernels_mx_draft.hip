@@ -14,7 +14,10 @@ namespace {
 // row that it points to has, and points it there, so that six rounds see 64
 // generations, fewer where the trees are shallower.  What lies before comes
 // from the words already done, in LDS.  The wave of word 0 counts ancestors
-// in the same rounds.
+// in the same rounds.  Bound by latency, a launch and its loads for the usual
+// draft (64 of 20 to 60 rows: 3.1 us) and some 0.6 us for every 64 rows of a
+// long one (16 of 300 to 1000 rows: 12.7 us; four times 64 rows in the same
+// rounds 13.2, eight words leaving together from LDS 15.8).
 __global__ __launch_bounds__(128) void k_mx_tree(const kvtc_mx_batch b, const int32_t* parents, uint32_t* masks, int words,
                                                  int32_t* positions, uint32_t* status, int most) {
   extern __shared__ uint32_t lds[];  // [2 waves][most] words, then [most] depths
@@ -63,11 +66,14 @@ __global__ __launch_bounds__(128) void k_mx_tree(const kvtc_mx_batch b, const in
 }
 
 // A workgroup lists the rows that stay, then its waves move the keys or the
-// values of some heads, sixteen tokens at a time: all of them are read before
-// any is written, and a token only moves down, so what is overwritten has
-// been read (the k-th kept row is row k or a later one).  Tokens that stay
-// where they are are not touched.
-template <int D, int BK, int BV>
+// values of HEADS (layer, head) pairs, 4 GROUPS tokens at a time: all of them
+// are read before any is written, and a token only moves down, so what is
+// overwritten has been read (the k-th kept row is row k or a later one).
+// Tokens that stay where they are are not touched.  Bound by latency: the
+// lengths, the mask, the pages, the codes (64 sequences of up to 8 rows, 32
+// layers x 8 heads: one pair a wave 13.4 us, four 9.9; a path of some hundred
+// rows through 10 pairs: 16 tokens at a time 13.4 us, 64 9.0).
+template <int D, int BK, int BV, int HEADS, int GROUPS>
 __global__ __launch_bounds__(256) void k_mx_keep(const MxKeepParams p) {
   constexpr MxRecord R = mx_record(D, BK, BV);
   constexpr int C = D / 16;
@@ -106,49 +112,66 @@ __global__ __launch_bounds__(256) void k_mx_keep(const MxKeepParams p) {
   const int kept = below[words], to0 = max(base, 0);
   if (tell && tid == 0) p.lens_out[z] = to0 + kept;
   const int32_t* table = p.b.page_table + (int64_t)z * p.b.max_pages;
-  const int w = __builtin_amdgcn_readfirstlane((int)(blockIdx.y * 4 + (tid >> 6)));
-  const int kv = w & 1, h = (w >> 1) % p.H, l = (w >> 1) / p.H;
-  if (l >= p.n_layers) return;
-  uint8_t* const head = p.pool + l * p.layer_bytes + (int64_t)h * R.bytes;
+  // this wave: keys or values of HEADS (layer, head) pairs
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), kv = wave & 1;
+  const int pair0 = ((int)blockIdx.y * 2 + (wave >> 1)) * HEADS, pairs = min(p.n_layers * p.H - pair0, HEADS);
+  if (pairs <= 0) return;
   const int64_t page_bytes = (int64_t)p.H * R.bytes;
   auto page_of = [&](int pos) {
     const int id = table[pos / KVTC_MX_PAGE];
     return (uint32_t)id < (uint32_t)p.pool_pages ? id : -1;
   };
+  uint8_t* head[HEADS];
+#pragma unroll
+  for (int j = 0; j < HEADS; ++j) {
+    const int pair = pair0 + min(j, pairs - 1), l = pair / p.H;
+    head[j] = p.pool + l * p.layer_bytes + (int64_t)(pair - l * p.H) * R.bytes;
+  }
   bool bad = false;
   auto move = [&](auto bits) {
     constexpr int B = decltype(bits)::value;
-    uint8_t* const codes = head + (kv ? R.kc : 0);
-    uint8_t* const scales = head + R.kc + R.vc + (kv ? R.sc : 0);
-    for (int k0 = 0; k0 < kept; k0 += 16) {
-      uint32_t c[4][2], sc[4];
-      int64_t to[4];
-      int at[4];
+    const int codes = kv ? R.kc : 0, scales = R.kc + R.vc + (kv ? R.sc : 0);
+    for (int k0 = 0; k0 < kept; k0 += 4 * GROUPS) {
+      int64_t from[GROUPS], to[GROUPS];  // the lane's codes of its tokens; from -1: nothing to move
+      int from_sc[GROUPS], to_sc[GROUPS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < GROUPS; ++i) {
         const int k = k0 + 4 * i + t4;
-        at[i] = -1;
-        c[i][0] = c[i][1] = sc[i] = 0;
-        to[i] = 0;
+        from[i] = to[i] = -1;
+        from_sc[i] = to_sc[i] = 0;
         if (k >= kept || base + row[k] == to0 + k) continue;
-        const int from = base + row[k], src = page_of(from), dst = page_of(to0 + k);
+        const int a = base + row[k], b = to0 + k, src = page_of(a), dst = page_of(b);
         if (src < 0 || dst < 0) {
           bad = true;
           continue;
         }
-        at[i] = (to0 + k) % KVTC_MX_PAGE;
-        to[i] = dst * page_bytes;
-        const int f = from % KVTC_MX_PAGE;
-        load_codes<B, C>(codes + src * page_bytes + code_at<D, B>(kv, f >> 2, f & 3, n), c[i]);
-        sc[i] = scales[src * page_bytes + scale_at<D>(kv, f >> 2, f & 3, n / (32 / C))];
+        const int ka = a % KVTC_MX_PAGE, kb = b % KVTC_MX_PAGE, ca = code_at<D, B>(kv, ka >> 2, ka & 3, n),
+                  cb = code_at<D, B>(kv, kb >> 2, kb & 3, n);
+        from[i] = src * page_bytes + codes + ca;
+        to[i] = dst * page_bytes + codes + cb;
+        from_sc[i] = scales + scale_at<D>(kv, ka >> 2, ka & 3, n / (32 / C)) - codes - ca;  // beside the codes
+        to_sc[i] = scales + scale_at<D>(kv, kb >> 2, kb & 3, n / (32 / C)) - codes - cb;
       }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // all sixteen have been read
+      uint32_t c[HEADS][GROUPS][2], sc[HEADS][GROUPS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (at[i] < 0) continue;
-        store_codes<B, C>(codes + to[i] + code_at<D, B>(kv, at[i] >> 2, at[i] & 3, n), c[i]);
-        if (n % (32 / C) == 0) scales[to[i] + scale_at<D>(kv, at[i] >> 2, at[i] & 3, n / (32 / C))] = (uint8_t)sc[i];
-      }
+      for (int j = 0; j < HEADS; ++j)
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+          c[j][i][0] = c[j][i][1] = sc[j][i] = 0;
+          if (from[i] >= 0 && j < pairs) {
+            load_codes<B, C>(head[j] + from[i], c[j][i]);
+            sc[j][i] = head[j][from[i] + from_sc[i]];
+          }
+        }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // all of them have been read
+#pragma unroll
+      for (int j = 0; j < HEADS; ++j)
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i)
+          if (from[i] >= 0 && j < pairs) {
+            store_codes<B, C>(head[j] + to[i], c[j][i]);
+            if (n % (32 / C) == 0) head[j][to[i] + to_sc[i]] = (uint8_t)sc[j][i];
+          }
     }
   };
   if (kv) move(std::integral_constant<int, BV>{});
@@ -158,8 +181,11 @@ __global__ __launch_bounds__(256) void k_mx_keep(const MxKeepParams p) {
 
 template <int D, int BK, int BV>
 hipError_t launch_keep(const MxKeepParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)p.b.n_seqs, (unsigned)((p.n_layers * p.H * 2 + 3) / 4));
-  k_mx_keep<D, BK, BV><<<grid, 256, 0, s>>>(p);
+  const unsigned pairs = (unsigned)(p.n_layers * p.H);
+  // where that leaves waves for every pair, long paths go in larger steps
+  if ((int64_t)pairs * p.b.n_seqs <= 2048)
+    k_mx_keep<D, BK, BV, 1, 16><<<dim3((unsigned)p.b.n_seqs, (pairs + 1) / 2), 256, 0, s>>>(p);
+  else k_mx_keep<D, BK, BV, 4, 4><<<dim3((unsigned)p.b.n_seqs, (pairs + 7) / 8), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 

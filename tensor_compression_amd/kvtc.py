@@ -847,7 +847,13 @@ class MxCache:
         return sh, st[0] if sh[0] > 1 else 0
 
     def _attention(self, batch, q, shared_pages, scale, causal, layer, out, lse, ws, status, stream, masks=None):
-        (sh, q_stride), D, index = self._queries(q, batch), self._head[1], self._index
+        self._own(q)
+        if batch.index != self._index:
+            raise ValueError("a batch on another device than the cache")
+        sh, st, D, index = q.shape, q.stride(), self._head[1], self._index
+        if q.dtype != self.dtype or len(sh) != 3 or sh[0] != batch.total_rows or sh[2] != D or st[2] != 1 or \
+                (st[1] != D and sh[1] > 1):
+            raise ValueError(f"queries are {self.dtype} [total_rows, heads, {D}] with contiguous heads")
         heads = sh[1]
         if out is None or ws is None:
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
@@ -866,13 +872,14 @@ class MxCache:
             lp = lse.data_ptr()
         if ws.get_device() != index or not ws.is_contiguous():
             raise ValueError("the workspace is a contiguous tensor on the cache's device")
-        head = (q.data_ptr(), q_stride, heads, scale if scale is not None else D ** -0.5)
-        tail = (out.data_ptr(), lp, ws.data_ptr(), ws.nbytes, self._status(status))
         if masks is not None:
             self._call(self._lib.kvtc_mx_attn_tree, stream, self._ref, batch.ref, layer, self._pool_ptr,
-                       self.pool_bytes, shared_pages, *self._masks(masks, batch), *head, *tail)
+                       self.pool_bytes, shared_pages, *self._masks(masks, batch), q.data_ptr(),
+                       st[0] if sh[0] > 1 else 0, heads, scale if scale is not None else D ** -0.5, out.data_ptr(), lp,
+                       ws.data_ptr(), ws.nbytes, self._status(status))
             return (out, lse) if lse is not None else out
-        tail = (*head, 1 if causal else 0, *tail)
+        tail = (q.data_ptr(), st[0] if sh[0] > 1 else 0, heads, scale if scale is not None else D ** -0.5,
+                1 if causal else 0, out.data_ptr(), lp, ws.data_ptr(), ws.nbytes, self._status(status))
         if shared_pages is None:
             self._call(self._lib.kvtc_mx_attn, stream, self._ref, batch.ref, layer, self._pool_ptr, self.pool_bytes,
                        *tail)
