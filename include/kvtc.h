@@ -732,7 +732,8 @@ enum { KVTC_MX_MAX_DRAFT = 4096 };
  * masks: device [total_rows][words]: the row itself and its ancestors.
  * positions (device int32 [total_rows], may be NULL): kv_lens[z] - n + the
  * number of ancestors, what kvtc_mx_write_rope takes.  Rows of no sequence
- * are left as they are.  The page table is not read. */
+ * are left as they are.  The three arrays must not overlap (INVALID_ARG).
+ * The page table is not read. */
 kvtc_status kvtc_mx_tree(const kvtc_mx_batch* batch, const int32_t* parents, uint32_t* masks, int32_t words,
                          int32_t* positions, uint32_t* status_dev, hipStream_t stream);
 
@@ -754,7 +755,8 @@ kvtc_status kvtc_mx_attn_tree(const kvtc_mx_config* cfg, const kvtc_mx_batch* ba
  * in their order, as its tokens kv_lens[z] - n, kv_lens[z] - n + 1, ...; the
  * codes and scales of layers [layer, layer + n_layers) are moved down to
  * there, bit for bit.  nodes: device int32 [n_seqs]; -1: none stays.
- * lens_out (device int32 [n_seqs], not kv_lens): the lengths after it.  What
+ * lens_out (device int32 [n_seqs], apart from kv_lens and nodes, INVALID_ARG):
+ * the lengths after it.  Drafts lie in pages of their own sequence.  What
  * lies behind them in the pool may be anything.  A node outside the rows, a
  * sequence outside the bounds: reported, nothing moves, and lens_out is
  * kv_lens[z]; a token whose page, or whose new page, is outside the pool:

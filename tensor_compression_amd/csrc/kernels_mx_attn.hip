@@ -84,7 +84,7 @@ __global__ __launch_bounds__(256) void k_mx_join(const MxJoinParams p) {
 
 hipError_t launch_mx_attn(const MxAttnParams* prefix, const MxAttnParams* own, int D, int bk, int bv, bool f32,
                           hipStream_t s) {
-  return launch_any<false>(prefix, own, D, bk, bv, f32, s);
+  return D == 128 ? launch_any<128, false>(prefix, own, bk, bv, f32, s) : launch_any<64, false>(prefix, own, bk, bv, f32, s);
 }
 
 template <int D, bool F32>

@@ -15,6 +15,12 @@ constexpr int64_t kMaxGrid = (1 << 24) - 1;  // workgroups of 256 threads in a l
 
 bool misaligned(const void* p, unsigned to = 16) { return ((uintptr_t)p & (to - 1)) != 0; }
 
+// Whether n 4-byte words at a and m at b share any.
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + 4 * (uint64_t)m && y < x + 4 * (uint64_t)n;
+}
+
 kvtc_status check_config(const kvtc_mx_config* c) {
   if (!c) return KVTC_ERR_INVALID_ARG;
   if (c->layers < 1 || c->kv_heads < 1 || c->pool_pages < 1) return KVTC_ERR_INVALID_ARG;
@@ -439,6 +445,11 @@ kvtc_status kvtc_mx_tree(const kvtc_mx_batch* batch, const int32_t* parents, uin
   if (misaligned(parents, 4) || misaligned(positions, 4) || misaligned(status_dev, 4)) return KVTC_ERR_INVALID_ARG;
   if (nothing_to_do(*batch)) return KVTC_OK;
   if (!parents) return KVTC_ERR_INVALID_ARG;
+  // several waves read the parents while others write
+  const int64_t rows = batch->total_rows;
+  if (overlap(parents, rows, positions, rows) || overlap(parents, rows, masks, rows * words) ||
+      overlap(positions, rows, masks, rows * words))
+    return KVTC_ERR_INVALID_ARG;
   if (batch->n_seqs > kMaxGrid) return KVTC_ERR_UNSUPPORTED;
   return launch_mx_tree(*batch, parents, masks, words, positions, status_dev, stream) == hipSuccess ? KVTC_OK
                                                                                                   : KVTC_ERR_HIP;
@@ -470,8 +481,12 @@ kvtc_status kvtc_mx_keep(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, 
   if (st != KVTC_OK) return st;
   if (misaligned(nodes, 4) || misaligned(lens_out, 4)) return KVTC_ERR_INVALID_ARG;
   if (batch->n_seqs == 0) return KVTC_OK;
-  if (!nodes || !lens_out || lens_out == batch->kv_lens) return KVTC_ERR_INVALID_ARG;
+  if (!nodes || !lens_out) return KVTC_ERR_INVALID_ARG;
   if (batch->n_seqs > kMaxGrid) return KVTC_ERR_UNSUPPORTED;
+  // every workgroup of a sequence reads its length and node
+  if (overlap(lens_out, batch->n_seqs, batch->kv_lens, batch->n_seqs) ||
+      overlap(lens_out, batch->n_seqs, nodes, batch->n_seqs))
+    return KVTC_ERR_INVALID_ARG;
   MxKeepParams p{};
   p.b = *batch;
   p.H = cfg->kv_heads;

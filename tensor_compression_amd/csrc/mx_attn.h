@@ -1169,14 +1169,10 @@ hipError_t launch_attn(const MxAttnParams* prefix, const MxAttnParams* own, bool
   return f32 ? launch_format<D, BK, BV, true, TREE>(prefix, own, s) : launch_format<D, BK, BV, false, TREE>(prefix, own, s);
 }
 
-template <bool TREE>
-hipError_t launch_any(const MxAttnParams* prefix, const MxAttnParams* own, int D, int bk, int bv, bool f32, hipStream_t s) {
-  if (D == 128) {
-    if (bk == 4) return bv == 4 ? launch_attn<128, 4, 4, TREE>(prefix, own, f32, s) : launch_attn<128, 4, 8, TREE>(prefix, own, f32, s);
-    return bv == 4 ? launch_attn<128, 8, 4, TREE>(prefix, own, f32, s) : launch_attn<128, 8, 8, TREE>(prefix, own, f32, s);
-  }
-  if (bk == 4) return bv == 4 ? launch_attn<64, 4, 4, TREE>(prefix, own, f32, s) : launch_attn<64, 4, 8, TREE>(prefix, own, f32, s);
-  return bv == 4 ? launch_attn<64, 8, 4, TREE>(prefix, own, f32, s) : launch_attn<64, 8, 8, TREE>(prefix, own, f32, s);
+template <int D, bool TREE>
+hipError_t launch_any(const MxAttnParams* prefix, const MxAttnParams* own, int bk, int bv, bool f32, hipStream_t s) {
+  if (bk == 4) return bv == 4 ? launch_attn<D, 4, 4, TREE>(prefix, own, f32, s) : launch_attn<D, 4, 8, TREE>(prefix, own, f32, s);
+  return bv == 4 ? launch_attn<D, 8, 4, TREE>(prefix, own, f32, s) : launch_attn<D, 8, 8, TREE>(prefix, own, f32, s);
 }
 
 }  // namespace

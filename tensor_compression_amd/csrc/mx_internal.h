@@ -77,6 +77,8 @@ hipError_t launch_mx_attn(const MxAttnParams* prefix, const MxAttnParams* own, i
                           hipStream_t s);
 hipError_t launch_mx_attn_tree(const MxAttnParams* prefix, const MxAttnParams* own, int D, int bk, int bv, bool f32,
                                hipStream_t s);
+hipError_t launch_mx_attn_tree64(const MxAttnParams* prefix, const MxAttnParams* own, int bk, int bv, bool f32,
+                                 hipStream_t s);
 hipError_t launch_mx_join(const MxJoinParams& p, bool f32, hipStream_t s);
 
 constexpr int kMxRopeSlice = 8;  // row vectors of a workgroup

@@ -245,6 +245,24 @@ def test_rope_slices_and_steps():
     assert torch.equal(c.cache.pool, want) and c.status.item() == 0
 
 
+@pytest.mark.parametrize("H,heads", [(9, 18), (8, 8), (17, 17), (1, 23)])
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+def test_rope_many_heads(H, heads, dtype):
+    """More vectors than a workgroup takes, part of a workgroup's, full pages
+    and parts of pages."""
+    for D, half in ((64, True), (128, False), (128, True)):
+        rows, lens = [45, 16, 1, 7], [50, 32, 33, 20]
+        c = Case(D, 4, 8, dtype, H, rows, lens, seed=H + D)
+        k, v, q = c.rand(c.total, H, D), c.rand(c.total, H, D), c.rand(c.total, heads, D)
+        out = c.cache.write_rope(c.batch, k, v, rope_of(D, half), q=q, status=c.status)
+        pos, axis = [own_positions(c)], [0] * (D // 2)
+        want = np.full(c.cache.pool.shape[1:], 0xFF, np.uint8)
+        mx_ref.write(want, c.table, lens, c.starts, mx_ref.rotate(np64(k), pos, freqs_of(D), axis, half), np64(v), D, 4, 8)
+        assert np.array_equal(c.cache.pool[0].cpu().numpy(), want)
+        check_queries(q, out, pos, D, half, axis, dtype, f"heads {H} {heads} D{D}")
+        assert c.status.item() == 0
+
+
 def test_rope_reports_and_skips():
     """Pages outside the pool, bad lengths: reported, nothing written there,
     queries of good sequences rotated; NaN and infinite frequencies."""
@@ -504,6 +522,48 @@ def test_tree_attention_nan_tokens(rows, G, dtype):
         c.cache.write(one, k[None], v[None])
 
 
+@pytest.mark.parametrize("G,most", [(4, 16), (8, 7)])
+def test_tree_attention_longest_first(G, most):
+    """More sequences in two tiles of 32 rows than the card holds at once: they
+    are taken by length; some without rows, some without tokens, some equal."""
+    n, H, D = 36, 8, 64
+    rng = np.random.default_rng(G)
+    lens = [int(x) for x in rng.integers(0, 2101, n)]
+    rows = [int(x) for x in rng.integers(0, most + 1, n)]
+    lens[0], lens[5], lens[6], lens[7], rows[0], rows[7] = 2100, 0, 1, 2100, most, most
+    c = Case(D, 8, 4, kvtc.BF16, H, [1], [2100], seed=G)
+    c.fill()
+    c.table_dev, c.table = c.table_dev.expand(n, -1).contiguous(), c.table * n
+    c.lens, c.rows, c.starts, c.total = lens, rows, [0] + [int(x) for x in np.cumsum(rows)], sum(rows) + 1
+    c.batch = c.new_batch(rows, lens, max_rows=most)
+    seen, masks = random_masks(c, "tree")
+    q, out, lse, scale = run_tree(c, G, masks)
+    check_tree_attention(c, q, out, lse, scale, seen, f"by length G{G}")
+
+
+@pytest.mark.parametrize("rows", [[2, 3, 1], [20, 30, 25]])
+def test_tree_attention_nan_in_the_prefix(rows):
+    """A NaN value in the shared prefix reaches the rows that are past it, in
+    its channels, and a sequence inside the prefix that ends before it not."""
+    D, G, shared = 128, 4, 4
+    lens = [64 + rows[0] + 5, 30 + rows[1], 64 + rows[2]]
+    lens[1] = min(lens[1], 40)
+    rows = [rows[0], min(rows[1], 12), rows[2]]
+    c = Case(D, 8, 8, kvtc.BF16, 2, rows, lens, seed=4, shared=shared)
+    c.fill()
+    seen, masks = random_masks(c, "tree")
+    q, good, _, _ = run_tree(c, G, masks, shared)
+    at, _, so = mx_ref.places(D, 8, 8, 1)
+    page, t = c.table[0][3], 10  # token 58
+    c.cache.pool[0, page, 1, int(so[t, 2])] = 255  # channels 64 to 95 of kv head 1
+    out = c.cache.attention_tree(c.batch, q, masks, shared)
+    nan = torch.isnan(out)
+    hit = torch.zeros_like(nan)
+    for z in (0, 2):
+        hit[c.starts[z]:c.starts[z + 1], G:, 64:96] = True
+    assert torch.equal(nan, hit) and torch.equal(out[~hit], good[~hit])
+
+
 def test_tree_attention_of_a_chain_is_causal():
     """A draft without branches, and a full mask, against the attentions that
     the cache had before: the same result within the bounds of both."""
@@ -593,6 +653,24 @@ def test_keep(D, bk, bv):
             out = c.cache.keep(c.batch, dev(nodes, torch.int32), masks, layer=layer, layers=layers, status=c.status)
             assert c.status.item() == 0
             check_keep(c, seen, nodes, before, out, list(range(layer, 3 if layers is None else layer + layers)))
+
+
+def test_keep_many_heads():
+    """Enough heads, layers and sequences that a wave takes several (layer,
+    head) pairs, the last of them fewer."""
+    rows, lens = [5, 1, 17, 0, 40, 6, 33, 3], [5, 20, 40, 9, 60, 4, 37, 0]
+    for D, bk, bv in ((64, 8, 4), (128, 4, 4)):
+        c = Case(D, bk, bv, kvtc.BF16, 7, rows, lens, layers=43, seed=D)
+        assert 43 * 7 * len(rows) > 2048
+        c.cache.pool.copy_(torch.as_tensor(c.rng.integers(0, 256, tuple(c.cache.pool.shape)), dtype=torch.uint8))
+        for kind in ("tree", "any"):
+            seen, masks = random_masks(c, kind)
+            nodes = [int(c.rng.integers(-1, max(n, 1))) for n in rows]
+            nodes[4], nodes[6] = 39, 32
+            before = c.cache.pool.cpu().numpy()
+            out = c.cache.keep(c.batch, dev(nodes, torch.int32), masks, status=c.status)
+            assert c.status.item() == 0
+            check_keep(c, seen, nodes, before, out, list(range(43)))
 
 
 def test_keep_long_paths():

@@ -24,7 +24,7 @@ def call(name, c=None, b=None, r=None, **kw):
     c, b, r = c or cfg(), b or batch(), r or rope()
     a = dict(layer=0, n_layers=1, positions=P, k=P, ks=strides(0, 128, 512), v=P, vs=strides(0, 128, 512), q=P, q_stride=1024,
              q_heads=8, q_out=P + 4096, q_out_stride=1024, pool=P, pool_bytes=1 << 40, status=P, masks=P, words=1, shared=2,
-             scale=0.1, out=P, lse=P, ws=P, ws_bytes=1 << 40, nodes=P, lens_out=P + 64, parents=P, tree_positions=P)
+             scale=0.1, out=P, lse=P, ws=P, ws_bytes=1 << 40, nodes=P, lens_out=P + 64, parents=P + 8192, tree_positions=P + 12288)
     a.update(kw)
     L, cr, br = kvtc.lib(), ctypes.byref(c), ctypes.byref(b)
     if name == "rope":
@@ -151,9 +151,10 @@ def test_bad_masks(name):
 
 
 def test_bad_trees_and_nodes():
-    for bad in (dict(parents=None), dict(parents=P + 2), dict(tree_positions=P + 2), dict(status=P + 1)):
+    for bad in (dict(parents=None), dict(parents=P + 2), dict(tree_positions=P + 2), dict(status=P + 1), dict(parents=P + 12288),
+                dict(parents=P + 12304), dict(masks=P + 8208), dict(masks=P + 12288 - 4 * 4)):
         assert call("tree", **bad) == INV, bad
-    for bad in (dict(nodes=None), dict(nodes=P + 2), dict(lens_out=None), dict(lens_out=P + 2), dict(lens_out=P),
+    for bad in (dict(nodes=None), dict(nodes=P + 2), dict(lens_out=None), dict(lens_out=P + 2), dict(lens_out=P), dict(lens_out=P + 8), dict(nodes=P + 128, lens_out=P + 120),
                 dict(n_layers=0), dict(n_layers=3), dict(layer=1, n_layers=2)):
         assert call("keep", **bad) == INV, bad
     for name in ("tree", "keep"):
