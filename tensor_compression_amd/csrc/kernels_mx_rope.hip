@@ -14,11 +14,12 @@
 // and the next one's loads under way 32 layers x 8 heads x 4096 tokens x 128
 // took 255 us, with four vectors loaded at once 148, with eight 133.
 //
-// Bound by memory: those (bf16, 4-bit codes, 680 MB) take 133 us (5.1 TB/s; the
+// Bound by memory: those (bf16, 4-bit codes, 680 MB) take 132 us (5.2 TB/s; the
 // write without rotation 117, a plain copy 5.1 TB/s), 15900 rows of prompts
-// with 32 query heads (370 MB) 87 us (4.2 TB/s; 92 with the queries' stores
-// through the caches); a step of 64 rows 5 us, the launch and five loads in a
-// row.  Vector instructions issue in 71% and 36% of the clocks.
+// with 32 query heads (385 MB) 88 us (4.4 TB/s; 92 with loads through the
+// caches, 96 with the queries' stores through them too); a step of 64 rows 5
+// us, the launch and five loads in a row.  Vector instructions issue in 73% and
+// 36% of the clocks.
 //
 // A key's codes have to be those of its rotation in fp64, so that is what it
 // is rotated in (products there are as fast as in fp32 on this card), and it
@@ -214,7 +215,8 @@ __global__ __launch_bounds__(256) void k_mx_rope(const MxRopeParams p) {
         } else {
 #pragma unroll
           for (int i = 0; i < W / 4; ++i) {
-            const uint4 u = on ? reinterpret_cast<const uint4*>(x)[i] : make_uint4(0, 0, 0, 0);
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (on) u = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4_out*>(x) + i));
             raw[c][4 * i] = u.x;
             raw[c][4 * i + 1] = u.y;
             raw[c][4 * i + 2] = u.z;
