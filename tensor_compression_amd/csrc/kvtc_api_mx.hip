@@ -430,7 +430,8 @@ kvtc_status kvtc_mx_write_rope(const kvtc_mx_config* cfg, const kvtc_mx_batch* b
   p.q_stride = q_stride;
   p.q_out_stride = q_out_stride;
   // (queries of rows before the first token too, so max_len is no bound here)
-  const int64_t units = std::max<int64_t>((std::min(batch->max_rows, batch->total_rows) + 2 * KVTC_MX_PAGE - 2) / KVTC_MX_PAGE, 1);
+  const int64_t rows = std::min(batch->max_rows, batch->total_rows);
+  const int64_t units = std::max<int64_t>((rows + 2 * KVTC_MX_PAGE - 2) / KVTC_MX_PAGE, 1);
   if (units * batch->n_seqs > kMaxGrid || parts * n_layers > 65535) return KVTC_ERR_UNSUPPORTED;
   p.io.n_units = (int32_t)units;
   return launch_mx_rope(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, cfg->dtype == KVTC_FP32, stream) == hipSuccess

@@ -141,6 +141,13 @@ def test_bad_rotated_rows():
     assert call("rope", c=cfg(layers=16384), n_layers=1, q_heads=2 ** 30 // 128, q_stride=2 ** 30, q_out_stride=2 ** 30) == UNS
 
 
+@pytest.mark.parametrize("rows", [2 ** 31 - 1, 2 ** 31 - 30, 2 ** 31 - 31])
+def test_rotated_rows_past_a_launch(rows):
+    """Row bounds at the end of int32: more pages than a launch has workgroups."""
+    for heads in (0, 8):
+        assert call("rope", b=batch(total_rows=rows, max_rows=rows), q_heads=heads) == UNS
+
+
 @pytest.mark.parametrize("name", ["attn", "keep", "tree"])
 def test_bad_masks(name):
     for bad, want in ((dict(masks=None), INV), (dict(masks=P + 2), INV), (dict(words=0), INV), (dict(words=-1), INV),
