@@ -69,7 +69,8 @@ __global__ __launch_bounds__(128) void k_mx_tree(const kvtc_mx_batch b, const in
 // values of HEADS (layer, head) pairs, 4 GROUPS tokens at a time: all of them
 // are read before any is written, and a token only moves down, so what is
 // overwritten has been read (the k-th kept row is row k or a later one).
-// Tokens that stay where they are are not touched.  Bound by latency: the
+// Tokens that stay where they are are not touched, but their pages are checked.
+// Bound by latency: the
 // lengths, the mask, the pages, the codes (64 sequences of up to 8 rows, 32
 // layers x 8 heads: one pair a wave 13.4 us, four 9.9; a path of some hundred
 // rows through 10 pairs: 16 tokens at a time 13.4 us, 64 9.0).
@@ -139,12 +140,13 @@ __global__ __launch_bounds__(256) void k_mx_keep(const MxKeepParams p) {
         const int k = k0 + 4 * i + t4;
         from[i] = to[i] = -1;
         from_sc[i] = to_sc[i] = 0;
-        if (k >= kept || base + row[k] == to0 + k) continue;
+        if (k >= kept) continue;
         const int a = base + row[k], b = to0 + k, src = page_of(a), dst = page_of(b);
         if (src < 0 || dst < 0) {
           bad = true;
           continue;
         }
+        if (a == b) continue;
         const int ka = a % KVTC_MX_PAGE, kb = b % KVTC_MX_PAGE, ca = code_at<D, B>(kv, ka >> 2, ka & 3, n),
                   cb = code_at<D, B>(kv, kb >> 2, kb & 3, n);
         from[i] = src * page_bytes + codes + ca;

@@ -717,6 +717,30 @@ def test_keep_reports_and_skips():
     assert np.array_equal(c.cache.pool.cpu().numpy(), want)
 
 
+def test_keep_reports_pages_of_tokens_that_stay():
+    """A path that keeps its place, as a draft accepted whole, or the first
+    part of one: a page outside the pool that a kept token stands in is
+    reported though nothing moves there; one of dropped rows alone is not."""
+    n, ln = 40, 70  # tokens 30 to 69: pages 1 (rows 0, 1) to 4 (rows 34 to 39)
+    first = list(range(20))  # rows 0 to 19, tokens 30 to 49: pages 1, 2 and two tokens of page 3
+    gap = first + [39]  # row 39 (page 4) moves to token 50, in page 3
+    seen = [[list(range(n)), first, gap] + [[i] for i in range(3, n)]]
+    for D, bk, bv, H, layers in ((64, 4, 8, 2, 1), (128, 8, 4, 8, 300)):  # one (layer, head) pair a wave, and four
+        c = Case(D, bk, bv, kvtc.BF16, H, [n], [ln], layers=layers, seed=D)
+        c.cache.pool.fill_(0x11)
+        masks = dev(mx_ref.mask_words(seen[0], 2), torch.int32)
+        for node, kept, pages in ((0, 40, (1, 2, 3, 4)), (1, 20, (1, 2, 3)), (2, 21, (1, 2, 3, 4))):
+            for page in (1, 2, 3, 4):
+                table = c.table_dev.clone()
+                table[0, page] = -1 if page % 2 else c.pages
+                b = c.cache.batch(table, c.batch.kv_lens, c.batch.row_start, total_rows=n, max_rows=n, max_len=ln)
+                before = c.cache.pool.clone()
+                out = c.cache.keep(b, dev([node], torch.int32), masks, status=c.status)
+                assert out.tolist() == [30 + kept] and c.status.item() == (INV if page in pages else 0), (node, page)
+                assert torch.equal(c.cache.pool, before)  # all bytes are alike
+                c.status.zero_()
+
+
 # ---- together
 
 
