@@ -755,8 +755,8 @@ kvtc_status kvtc_mx_attn_tree(const kvtc_mx_config* cfg, const kvtc_mx_batch* ba
  * in their order, as its tokens kv_lens[z] - n, kv_lens[z] - n + 1, ...; the
  * codes and scales of layers [layer, layer + n_layers) are moved down to
  * there, bit for bit.  nodes: device int32 [n_seqs]; -1: none stays.
- * lens_out (device int32 [n_seqs], apart from kv_lens and nodes, INVALID_ARG):
- * the lengths after it.  Drafts lie in pages of their own sequence.  What
+ * lens_out (device int32 [n_seqs], apart from the pool and all that is read,
+ * INVALID_ARG): the lengths after it.  Drafts lie in pages of their own sequence.  What
  * lies behind them in the pool may be anything.  A node outside the rows, a
  * sequence outside the bounds: reported, nothing moves, and lens_out is
  * kv_lens[z]; a token whose page, or whose new page, is outside the pool:

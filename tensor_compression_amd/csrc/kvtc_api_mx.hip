@@ -485,9 +485,12 @@ kvtc_status kvtc_mx_keep(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, 
   if (batch->n_seqs == 0) return KVTC_OK;
   if (!nodes || !lens_out) return KVTC_ERR_INVALID_ARG;
   if (batch->n_seqs > kMaxGrid) return KVTC_ERR_UNSUPPORTED;
-  // every workgroup of a sequence reads its length and node
-  if (overlap(lens_out, batch->n_seqs, batch->kv_lens, batch->n_seqs) ||
-      overlap(lens_out, batch->n_seqs, nodes, batch->n_seqs))
+  // every workgroup of a sequence reads its length, rows, node, mask and pages
+  const int64_t n = batch->n_seqs;
+  if (overlap(lens_out, n, batch->kv_lens, n) || overlap(lens_out, n, batch->row_start, n + 1) ||
+      overlap(lens_out, n, batch->page_table, n * batch->max_pages) || overlap(lens_out, n, nodes, n) ||
+      overlap(lens_out, n, masks, (int64_t)batch->total_rows * words) ||
+      overlap(lens_out, n, pool, cfg->layers * (layer_bytes(*cfg) / 4)))
     return KVTC_ERR_INVALID_ARG;
   MxKeepParams p{};
   p.b = *batch;

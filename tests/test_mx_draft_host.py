@@ -168,6 +168,36 @@ def test_bad_trees_and_nodes():
         assert call(name, b=batch(n_seqs=2 ** 24)) == UNS
 
 
+def apart(**kw):
+    """The arrays of a batch of 3 sequences, 5 rows and 6 pages each, 64 KB apart."""
+    a = dict(page_table=P, kv_lens=P + 0x10000, row_start=P + 0x20000)
+    a.update(kw)
+    return batch(n_seqs=3, total_rows=5, max_rows=5, max_pages=6, max_len=96, **a)
+
+
+def launched(status):
+    """A call that nothing refused: without a GPU its launch fails."""
+    if torch.cuda.is_available():
+        pytest.skip("would be launched with these addresses")
+    return status == kvtc.ERR_HIP
+
+
+def test_kept_lengths_apart_from_what_is_read():
+    """The lengths after it overlap nothing that other workgroups still read,
+    and may lie right beside it."""
+    need = size(cfg())[2]
+    a = dict(masks=P + 0x30000, words=2, nodes=P + 0x40000, pool=P + 0x50000, pool_bytes=need)
+    # start and size of what is read
+    for at, n in ((P, 3 * 6 * 4), (P + 0x10000, 3 * 4), (P + 0x20000, 4 * 4), (P + 0x30000, 5 * 2 * 4), (P + 0x40000, 3 * 4),
+                  (P + 0x50000, need)):
+        for lens_out in (at, at + n - 4, at - 8, at - 4):
+            assert call("keep", b=apart(), lens_out=lens_out, **a) == INV, (hex(at), lens_out - at)
+    for at, n in ((P, 3 * 6 * 4), (P + 0x10000, 3 * 4), (P + 0x20000, 4 * 4), (P + 0x30000, 5 * 2 * 4), (P + 0x40000, 3 * 4),
+                  (P + 0x50000, need)):
+        for lens_out in (at - 12, at + n):
+            assert launched(call("keep", b=apart(), lens_out=lens_out, **a)), (hex(at), lens_out - at)
+
+
 def test_bad_tree_attention():
     for bad in (dict(q=None), dict(out=None), dict(q=P + 2), dict(out=P + 8), dict(lse=P + 2), dict(ws=P + 8),
                 dict(q_stride=-8), dict(q_stride=12), dict(q_heads=0), dict(q_heads=6), dict(scale=0.0), dict(scale=-1.0),
