@@ -732,8 +732,9 @@ enum { KVTC_MX_MAX_DRAFT = 4096 };
  * masks: device [total_rows][words]: the row itself and its ancestors.
  * positions (device int32 [total_rows], may be NULL): kv_lens[z] - n + the
  * number of ancestors, what kvtc_mx_write_rope takes.  Rows of no sequence
- * are left as they are.  The three arrays must not overlap (INVALID_ARG).
- * The page table is not read. */
+ * are left as they are.  masks and positions must not overlap each other,
+ * parents, or the batch's lengths and rows (INVALID_ARG).  The page table is
+ * not read. */
 kvtc_status kvtc_mx_tree(const kvtc_mx_batch* batch, const int32_t* parents, uint32_t* masks, int32_t words,
                          int32_t* positions, uint32_t* status_dev, hipStream_t stream);
 
@@ -756,13 +757,13 @@ kvtc_status kvtc_mx_attn_tree(const kvtc_mx_config* cfg, const kvtc_mx_batch* ba
  * codes and scales of layers [layer, layer + n_layers) are moved down to
  * there, bit for bit.  nodes: device int32 [n_seqs]; -1: none stays.
  * lens_out (device int32 [n_seqs], apart from the pool and all that is read,
- * INVALID_ARG): the lengths after it.  Drafts lie in pages of their own sequence.  What
- * lies behind them in the pool may be anything.  A node outside the rows, a
- * sequence outside the bounds: reported, nothing moves, and lens_out is
- * kv_lens[z]; a token whose page, or whose new page, is outside the pool:
- * reported and left out of the move.  Sequences without rows keep their
- * length.  Rows before the first token (more rows than tokens) hold no token
- * and are passed over. */
+ * INVALID_ARG): the lengths after it.  Drafts lie in pages of their own
+ * sequence.  What lies behind them in the pool may be anything.  A node
+ * outside the rows, a sequence outside the bounds: reported, nothing moves,
+ * and lens_out is kv_lens[z]; a token whose page, or whose new page, is
+ * outside the pool: reported and left out of the move.  Sequences without
+ * rows keep their length.  Rows before the first token (more rows than
+ * tokens) hold no token and are passed over. */
 kvtc_status kvtc_mx_keep(const kvtc_mx_config* cfg, const kvtc_mx_batch* batch, int32_t layer, int32_t n_layers,
                          const uint32_t* masks, int32_t words, const int32_t* nodes, void* pool, size_t pool_bytes,
                          int32_t* lens_out, uint32_t* status_dev, hipStream_t stream);

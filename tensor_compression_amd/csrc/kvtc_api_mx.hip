@@ -447,12 +447,15 @@ kvtc_status kvtc_mx_tree(const kvtc_mx_batch* batch, const int32_t* parents, uin
   if (misaligned(parents, 4) || misaligned(positions, 4) || misaligned(status_dev, 4)) return KVTC_ERR_INVALID_ARG;
   if (nothing_to_do(*batch)) return KVTC_OK;
   if (!parents) return KVTC_ERR_INVALID_ARG;
-  // several waves read the parents while others write
-  const int64_t rows = batch->total_rows;
-  if (overlap(parents, rows, positions, rows) || overlap(parents, rows, masks, rows * words) ||
-      overlap(positions, rows, masks, rows * words))
-    return KVTC_ERR_INVALID_ARG;
   if (batch->n_seqs > kMaxGrid) return KVTC_ERR_UNSUPPORTED;
+  // several waves read the parents, lengths and rows while others write
+  const int64_t rows = batch->total_rows, n = batch->n_seqs;
+  auto apart = [&](const void* out, int64_t words_out) {
+    return !overlap(out, words_out, parents, rows) && !overlap(out, words_out, batch->kv_lens, n) &&
+           !overlap(out, words_out, batch->row_start, n + 1);
+  };
+  if (!apart(positions, rows) || !apart(masks, rows * words) || overlap(positions, rows, masks, rows * words))
+    return KVTC_ERR_INVALID_ARG;
   return launch_mx_tree(*batch, parents, masks, words, positions, status_dev, stream) == hipSuccess ? KVTC_OK
                                                                                                   : KVTC_ERR_HIP;
 }

@@ -198,6 +198,23 @@ def test_kept_lengths_apart_from_what_is_read():
             assert launched(call("keep", b=apart(), lens_out=lens_out, **a)), (hex(at), lens_out - at)
 
 
+def test_masks_and_positions_apart_from_what_is_read():
+    """Neither overlaps the parents, lengths or rows of the batch, or each
+    other; they may lie right beside them.  The page table is not read."""
+    a = dict(parents=P + 0x30000, masks=P + 0x40000, words=2, tree_positions=P + 0x50000)
+    read = ((P + 0x10000, 3 * 4), (P + 0x20000, 4 * 4), (P + 0x30000, 5 * 4))  # lengths, rows, parents
+    for at, n in read + ((P + 0x40000, 5 * 2 * 4),):
+        for positions in (at, at + n - 4, at - 16, at - 4):
+            assert call("tree", b=apart(), **{**a, "tree_positions": positions}) == INV, (hex(at), positions - at)
+    for at, n in read + ((P + 0x50000, 5 * 4),):
+        for masks in (at, at + n - 4, at - 36, at - 4):
+            assert call("tree", b=apart(), **{**a, "masks": masks}) == INV, (hex(at), masks - at)
+    for at, n in read:
+        for positions, masks in ((at - 20, at + n), (at + n, at - 40)):
+            assert launched(call("tree", b=apart(), **{**a, "tree_positions": positions, "masks": masks})), hex(at)
+    assert launched(call("tree", b=apart(), **{**a, "masks": P})) and launched(call("tree", b=apart(), **{**a, "tree_positions": P}))
+
+
 def test_bad_tree_attention():
     for bad in (dict(q=None), dict(out=None), dict(q=P + 2), dict(out=P + 8), dict(lse=P + 2), dict(ws=P + 8),
                 dict(q_stride=-8), dict(q_stride=12), dict(q_heads=0), dict(q_heads=6), dict(scale=0.0), dict(scale=-1.0),
