@@ -703,8 +703,8 @@ typedef struct kvtc_mx_rope {
  * fp32 saturate.  Values are quantised as kvtc_mx_write does.  Queries are rotated
  * in fp32 (by cos and sin of the fp64 angle within 2.3 2^-24) and rounded once
  * to their type: element (r, h, c) from q + r q_stride + h head_dim + c to q_out +
- * r q_out_stride + h head_dim + c.  q_out may be q with the same stride; it
- * must not overlap the call's inputs otherwise.  q_heads 0: no queries, q and
+ * r q_out_stride + h head_dim + c.  q_out may be q with the same stride; its
+ * elements must not be the pool's or other inputs' (INVALID_ARG).  q_heads 0: no queries, q and
  * q_out are not looked at; else n_layers must be 1.  q_stride and
  * q_out_stride as in kvtc_mx_attn, q_out_stride at least q_heads head_dim.
  * Queries of rows before the first token (more rows than tokens) are rotated

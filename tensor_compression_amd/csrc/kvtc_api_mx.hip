@@ -21,6 +21,34 @@ bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
   return a && b && x < y + 4 * (uint64_t)m && y < x + 4 * (uint64_t)n;
 }
 
+// n rows of `bytes` bytes, `stride` bytes apart, and whether any of two such
+// tensors share a byte.
+struct RowBytes {
+  const void* at;
+  int64_t bytes, stride, n;
+};
+bool meet(RowBytes a, RowBytes b) {
+  for (RowBytes* x : {&a, &b})
+    if (x->n > 1 && x->stride <= x->bytes) {  // without gaps
+      x->bytes += (x->n - 1) * x->stride;
+      x->n = 1;
+    }
+  if (a.n < b.n) std::swap(a, b);
+  typedef __int128 wide;
+  const wide d = (wide)(uintptr_t)b.at - (wide)(uintptr_t)a.at;
+  if (d >= (wide)a.stride * (a.n - 1) + a.bytes || -d >= (wide)b.stride * (b.n - 1) + b.bytes) return false;
+  // row i of a meets one at x where x - a.bytes < i a.stride < x + b.bytes
+  auto some = [&](wide x, int64_t first, int64_t last) {
+    if (a.n == 1) return x < a.bytes && -x < b.bytes;
+    const wide low = x - a.bytes, i = low / a.stride - (low % a.stride < 0) + 1;
+    return std::max<wide>(i, first) <= last && std::max<wide>(i, first) * a.stride < x + b.bytes;
+  };
+  if (a.stride == b.stride) return some(d, 1 - b.n, a.n - 1);  // rows i and j: as i - j and 0
+  for (int64_t j = 0; j < b.n; ++j)
+    if (some(d + (wide)j * b.stride, 0, a.n - 1)) return true;
+  return false;
+}
+
 kvtc_status check_config(const kvtc_mx_config* c) {
   if (!c) return KVTC_ERR_INVALID_ARG;
   if (c->layers < 1 || c->kv_heads < 1 || c->pool_pages < 1) return KVTC_ERR_INVALID_ARG;
@@ -433,6 +461,22 @@ kvtc_status kvtc_mx_write_rope(const kvtc_mx_config* cfg, const kvtc_mx_batch* b
   const int64_t rows = std::min(batch->max_rows, batch->total_rows);
   const int64_t units = std::max<int64_t>((rows + 2 * KVTC_MX_PAGE - 2) / KVTC_MX_PAGE, 1);
   if (units * batch->n_seqs > kMaxGrid || parts * n_layers > 65535) return KVTC_ERR_UNSUPPORTED;
+  if (q_heads > 0) {  // what other workgroups still read
+    const int64_t D = cfg->head_dim * elem, n = batch->total_rows;
+    const RowBytes to{q_out, q_heads * D, q_out_stride * elem, n};
+    auto over = [&](const void* x, int64_t bytes) { return x && meet(to, RowBytes{x, bytes, 0, 1}); };
+    bool bad = (q != q_out && meet(to, RowBytes{q, q_heads * D, q_stride * elem, n})) || over(positions, n * rope->axes * 4) ||
+               over(rope->freqs, rope->rot_dim * 4) || over(batch->page_table, (int64_t)batch->n_seqs * batch->max_pages * 4) ||
+               over(batch->kv_lens, (int64_t)batch->n_seqs * 4) || over(batch->row_start, ((int64_t)batch->n_seqs + 1) * 4) ||
+               over(pool, cfg->layers * layer_bytes(*cfg));
+    for (int i = 0; i < 2; ++i) {
+      const int64_t head = p.io.st[i][1] * elem, row = p.io.st[i][2] * elem;
+      const int heads = head == D ? 1 : cfg->kv_heads;  // side by side: as one
+      for (int h = 0; h < heads; ++h)
+        bad |= meet(to, RowBytes{(const uint8_t*)p.io.x[i] + h * head, D * (cfg->kv_heads / heads), row, n});
+    }
+    if (bad) return KVTC_ERR_INVALID_ARG;
+  }
   p.io.n_units = (int32_t)units;
   return launch_mx_rope(p, cfg->head_dim, cfg->bits_k, cfg->bits_v, cfg->dtype == KVTC_FP32, stream) == hipSuccess
              ? KVTC_OK

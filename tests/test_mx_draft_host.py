@@ -148,6 +148,56 @@ def test_rotated_rows_past_a_launch(rows):
         assert call("rope", b=batch(total_rows=rows, max_rows=rows), q_heads=heads) == UNS
 
 
+def test_rotated_queries_apart_from_what_is_read():
+    """Slices of any strides and heads near each other: refused exactly where
+    a written element is one that the call reads, but for queries in place."""
+    rng = np.random.default_rng(11)
+    D, unit = 64, 8  # elements of 2 bytes, strides in whole 16 bytes
+
+    def taken(at, strides, extent):  # 16-byte units
+        i = np.add.outer(np.arange(extent[0]) * strides[0], np.arange(extent[1]) * strides[1])
+        return set((at // 16 + np.add.outer(i.ravel() // unit, np.arange(D // unit))).ravel().tolist())
+
+    def some(*choices):
+        return int(rng.choice(choices))
+
+    seen = [0, 0, 0]
+    for trial in range(3000):
+        rows, H, G = some(1, 2, 5), some(1, 2), some(1, 2, 3)
+        fused = (G + 2) * H * D
+        qw = G * H * D
+        qs, os = some(0, qw, fused, fused, qw + 8, 2 * qw), some(qw, fused, fused, 2 * qw, qw + 24)
+        ks = [(D, fused), (D, fused), (D, H * D), (rows * D, D), (0, D), (D, 0), (D + 8, 3 * D + 8)][some(*range(7))]
+        base = P + 0x100000
+        q = base + 16 * some(0, 0, 0, *range(0, 200, 7))
+        q_out = q if trial % 3 == 0 else base + 16 * some(*range(-60, 260))
+        k = q + 2 * qw if trial % 2 else base + 16 * some(*range(-100, 300))
+        v = k + 2 * H * D if trial % 5 else base + 16 * some(*range(2000, 2500))
+        out = taken(q_out, (os, D), (rows, G * H))
+        b = batch(n_seqs=1, total_rows=rows, max_rows=rows, page_table=P, kv_lens=P + 0x10000, row_start=P + 0x20000)
+        bad = q == q_out and qs != os  # in place: the same strides
+        bad |= q != q_out and bool(out & taken(q, (qs, D), (rows, G * H)))
+        bad |= any(out & taken(x, (ks[1], ks[0]), (rows, H)) for x in (k, v))
+        got = call("rope", c=cfg(head_dim=D, kv_heads=H), b=b, r=rope(rot_dim=D, freqs=P + 0x30000), positions=P + 0x40000, k=k, v=v,
+                   ks=strides(0, *ks), vs=strides(0, *ks), q=q, q_stride=qs, q_heads=G * H, q_out=q_out, q_out_stride=os,
+                   pool=P + 0x8000000)
+        assert got == INV if bad else launched(got), (trial, rows, H, G, qs, os, ks, q - base, q_out - base, k - base, v - base)
+        seen[2 if bad else q == q_out] += 1
+    assert min(seen) > 100, seen  # of each kind
+
+
+def test_rotated_queries_apart_from_small_inputs_and_the_pool():
+    need = size(cfg())[2]
+    b = batch(n_seqs=3, total_rows=5, max_rows=5, page_table=P, kv_lens=P + 0x10000, row_start=P + 0x20000)
+    for at, n in ((P, 3 * 6 * 4), (P + 0x10000, 3 * 4), (P + 0x20000, 4 * 4), (P + 0x30000, 64 * 8), (P + 0x40000, 2 * 5 * 4),
+                  (P + 0x8000000, need)):
+        last = at + n - 1 - (at + n - 1) % 16
+        for q_out, want in ((at, INV), (last, INV), (at - 5 * 8 * 128 * 2 + 16, INV), (at - 5 * 8 * 128 * 2, None), (last + 16, None)):
+            got = call("rope", b=b, r=rope(freqs=P + 0x30000, axes=2, axis=bytes([0, 1] * 32)), positions=P + 0x40000, k=P + 0x1000000,
+                       v=P + 0x2000000, q=P + 0x3000000, q_out=q_out, pool=P + 0x8000000, pool_bytes=need)
+            assert got == INV if want else launched(got), (hex(at), q_out - at)
+
+
 @pytest.mark.parametrize("name", ["attn", "keep", "tree"])
 def test_bad_masks(name):
     for bad, want in ((dict(masks=None), INV), (dict(masks=P + 2), INV), (dict(words=0), INV), (dict(words=-1), INV),
