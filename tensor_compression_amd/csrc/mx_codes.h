@@ -31,9 +31,8 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t a) {
   return (uint32_t)min(max(s, 15), B == 4 ? 252 : 246);
 }
 
-// C elements under scale 2^(s - 127): 4-bit codes in w[0], 8-bit codes four a
-// word.  CLAMPED false: the scale is not a clamped one.
-template <int B, int C, bool CLAMPED = true>
+// C elements under scale 2^(s - 127): 4-bit codes in w[0], 8-bit codes four a word.
+template <int B, int C>
 __device__ __forceinline__ void encode(const float (&x)[C], uint32_t s, uint32_t (&w)[2]) {
   const float sc = __uint_as_float(s << 23);
   if constexpr (B == 4) {
@@ -51,12 +50,6 @@ __device__ __forceinline__ void encode(const float (&x)[C], uint32_t s, uint32_t
 #pragma unroll
     for (int i = 0; i < C / 4; ++i) {
       s16x2_t o = {0, 0};
-      if constexpr (!CLAMPED) {
-        o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, x[4 * i], x[4 * i + 1], sc, false);
-        o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, x[4 * i + 2], x[4 * i + 3], sc, true);
-        w[i] = __builtin_bit_cast(uint32_t, o);
-        continue;
-      }
       o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, __builtin_amdgcn_fmed3f(x[4 * i], -top, top),
                                                    __builtin_amdgcn_fmed3f(x[4 * i + 1], -top, top), sc, false);
       o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, __builtin_amdgcn_fmed3f(x[4 * i + 2], -top, top),
