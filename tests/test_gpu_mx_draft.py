@@ -541,6 +541,65 @@ def test_tree_attention_longest_first(G, most):
     check_tree_attention(c, q, out, lse, scale, seen, f"by length G{G}")
 
 
+# How attention over drafts is cut up: (kv heads, query heads of each, sequences, most rows of one, longest, bound on
+# the lengths, shared pages).  Rows of a sequence and kv head: up to 16 in one tile, up to 64 in tiles of 32, else of
+# 128.  Eight waves a workgroup: one tile of 16, at most 256 workgroups, ranges of more than 512 tokens.  Past the
+# caches: under these bounds the smallest record (1088 bytes of 16 tokens and a head) passes 256 MB.  By length: more
+# than 256 / kv heads sequences and a bound of 2048 or more.
+CUTS = {
+    "16 rows": (2, 4, 9, 4, 500, 500, 0),
+    "16 rows, eight waves": (2, 4, 128, 4, 600, 600, 0),
+    "16 rows, eight waves, past the caches": (2, 4, 128, 4, 600, 16384, 0),
+    "16 rows, eight waves, ranges": (32, 1, 1, 5, 4500, 4500, 0),
+    "16 rows, eight waves, ranges, past the caches": (32, 1, 1, 5, 4500, 131072, 0),
+    "16 rows, by length": (2, 4, 136, 4, 2100, 2100, 0),
+    "16 rows, by length, past the caches": (2, 4, 136, 4, 700, 16384, 0),
+    "16 rows, ranges": (2, 4, 3, 4, 2100, 2100, 0),
+    "32 rows": (2, 4, 9, 16, 700, 700, 0),
+    "32 rows, ranges": (2, 4, 2, 16, 2100, 2100, 0),
+    "128 rows, ranges": (2, 4, 1, 40, 2100, 2100, 0),
+    "prefix of 128 rows beside 16": (2, 4, 20, 4, 800, 800, 32),
+    "prefix of 128 rows, 16 past the caches": (2, 4, 20, 4, 800, 131072, 32),
+    "prefix of 128 rows, then 32": (2, 4, 9, 16, 800, 800, 32),
+    "prefix of 128 rows beside 128": (2, 4, 6, 33, 800, 800, 32),
+    "prefix of 32 rows, then 16": (2, 4, 4, 4, 800, 800, 32),
+    "prefix of 16 rows": (2, 2, 2, 4, 800, 800, 32),
+}
+
+
+@pytest.mark.parametrize("cut", CUTS)
+@pytest.mark.parametrize("dtype", [kvtc.BF16, kvtc.FP32])
+@pytest.mark.parametrize("D,bk,bv", FORMATS)
+def test_tree_attention_cuts(D, bk, bv, dtype, cut):
+    """Every way that a call is cut up, in every format and type.  All
+    sequences lie in the same pages; table entries from the longest on are
+    outside the pool."""
+    H, G, n, most, longest, bound, shared = CUTS[cut]
+    rng = np.random.default_rng(n + D + bk)
+    least = 16 * shared
+    lens = [int(x) for x in rng.integers(least, longest + 1, n)]
+    rows = [int(x) for x in rng.integers(0, most + 1, n)]
+    lens[0], rows[0] = longest, most
+    if n > 1:
+        rows[1] = most
+    if n > 3:
+        lens[2], lens[3], rows[2], rows[3] = max(least - 5, 0), 1, 1, 1
+    if n > 6:
+        lens[4], rows[4], lens[6] = 0, 2, lens[5]
+    c = Case(D, bk, bv, dtype, H, [1], [longest], seed=D + bv)
+    c.fill()
+    width = -(-bound // 16)
+    assert (n * (bound - least) * H * (D * (bk + bv) // 8 + D // 16) > 2 ** 28) == ("past" in cut)
+    c.table_dev = torch.cat([c.table_dev[:, :-1], c.table_dev[:, -1:].expand(1, width)], 1)[:, :width].expand(n, -1).contiguous()
+    c.table = c.table * n
+    c.lens, c.rows, c.starts, c.total = lens, rows, [0] + [int(x) for x in np.cumsum(rows)], sum(rows) + 1
+    c.batch = c.new_batch(rows, lens, max_rows=most, max_len=bound)
+    seen, masks = random_masks(c, "any" if (bk == 4) == (bv == 4) else "tree")
+    print("cut", cut, D, bk, bv, dtype, flush=True)
+    q, out, lse, scale = run_tree(c, G, masks, shared)
+    check_tree_attention(c, q, out, lse, scale, seen, f"{cut} D{D} k{bk} v{bv} dtype {dtype}")
+
+
 @pytest.mark.parametrize("rows", [[2, 3, 1], [20, 30, 25]])
 def test_tree_attention_nan_in_the_prefix(rows):
     """A NaN value in the shared prefix reaches the rows that are past it, in
