@@ -254,15 +254,18 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
     a->together = a->prefix.nt == 8 && a->own.nt == 1 && !a->once;
     if (a->together) a->own.waves = 4;
     // Drafts: also where both take the kernel for many rows (32 sequences of 10
-    // to 25 rows behind 8192: 121 us a call one after the other, 103 to 110 so).
+    // to 25 rows behind 8192: 125 us a call one after the other, 109 so; fp32
+    // 260 and 230).  Rows without masks were not timed this way, and have no
+    // such kernel.
     if (tree && a->prefix.nt == 8 && a->own.nt == 8 &&
         (a->own.tiles * a->own.nsplit * b.n_seqs + a->prefix.tiles * a->prefix.nsplit) * c.kv_heads <= kMaxGrid)
       a->together = true;
   }
   a->slots = a->begin > 0 || a->own.nsplit > 1 ? a->prefix.nsplit + a->own.nsplit : 0;
   a->ws = a->slots * b.total_rows * q_heads * (int64_t)(c.head_dim + 2) * 4;
-  // (each its own launch; in one they have at most 256 MB of own codes, so
-  // fewer than 2^22 workgroups of own tokens, and 2^20 of the prefix)
+  // (each its own launch; in one, own tokens on 16-row tiles have at most 256
+  // MB of codes, so fewer than 2^22 workgroups, and the prefix 2^20; the
+  // drafts' 128-row tiles of both were added up above)
   if (a->own.tiles * c.kv_heads * std::max(a->own.nsplit, 1) * b.n_seqs > kMaxGrid ||
       a->prefix.tiles * c.kv_heads * std::max(a->prefix.nsplit, 1) > kMaxGrid ||
       (int64_t)b.total_rows * q_heads > 4 * kMaxGrid)
@@ -272,9 +275,9 @@ kvtc_status plan_attn(const kvtc_mx_config& c, const kvtc_mx_batch& b, int32_t q
 
 // masks: rows are drafts (then causal is 0).
 kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t layer, const void* pool,
-                      size_t pool_bytes, int32_t shared, const uint32_t* masks, int32_t words, const void* q, int64_t q_stride, int32_t q_heads, float scale,
-                      int32_t causal, void* out, float* lse, void* ws, size_t ws_bytes, uint32_t* status,
-                      hipStream_t stream) {
+                      size_t pool_bytes, int32_t shared, const uint32_t* masks, int32_t words, const void* q,
+                      int64_t q_stride, int32_t q_heads, float scale, int32_t causal, void* out, float* lse, void* ws,
+                      size_t ws_bytes, uint32_t* status, hipStream_t stream) {
   uint8_t* first;
   kvtc_status st = check_call(cfg, b, layer, 1, pool, pool_bytes, status, &first);
   if (st != KVTC_OK) return st;
@@ -337,7 +340,9 @@ kvtc_status attn_call(const kvtc_mx_config* cfg, const kvtc_mx_batch* b, int32_t
     p.pair = (int32_t)per_round;
   // Drafts in two tiles of 32 rows, more workgroups than the card holds at once
   // (two a unit): the longest sequences first (64 of 511 to 8191 tokens, 5 to
-  // 16 rows of 4 heads each: 141 -> 112 us).
+  // 16 rows of 4 heads each: 141 -> 112 us).  The longest takes as long as the
+  // call (8064 tokens, an even share is 6795).  Rows without masks were not
+  // timed in this order, and keep that of the batch.
   if (masks && !a.prefix.nsplit && a.own.nt == 2 && a.own.tiles > 1 && a.own.nsplit == 1 &&
       a.own.tiles * cfg->kv_heads * b->n_seqs > 512 && b->n_seqs <= 256 && b->max_len >= 2048)
     p.pair = 1;

@@ -751,8 +751,10 @@ __global__ __launch_bounds__(W * 64, W == 4 && NT == 1 && !F32 ? 3 : 2) void k_m
 // smallest parts of all but 16 channels go to LDS, as many as leave room for
 // two workgroups a CU, and one tile's codes are on their way instead of three
 // (2048 rows on 4096 tokens: k4v4 545 -> 490 us, k8v8 706 -> 455; 64 channels
-// fit: 241 us, 250 this way).  It is still 9 (k4v4) to 12 registers too many,
-// which are spilled: 40 to 52 bytes of scratch a lane.
+// fit: 241 us, 250 this way).  k4v4 fits so, the other formats are still 1 to 5
+// registers too many (8 to 24 bytes of scratch a lane; with masks up to 3, both
+// passes of drafts in one launch up to 9).  An earlier form, with 9 to 12
+// spilled, took the same beside it on one card: 411 (k4v4) to 425 us (k8v8).
 template <int D, bool F32>
 constexpr bool many_tight = F32 && D == 128;
 template <int D, bool F32>
@@ -1111,8 +1113,8 @@ __global__ __launch_bounds__(256, 2) void k_mx_rows(const MxAttnParams p) {
 
 // Drafts of many rows behind a shared prefix: both passes in one launch, so
 // that the short own ranges fill what the prefix's leave (32 sequences of 10
-// to 25 rows and 4 heads behind 8192, with the join: 121 us one after the
-// other, 103 to 110 so).
+// to 25 rows and 4 heads behind 8192, a call with its join: 125 us one after
+// the other, 109 so; fp32 260 and 230).
 template <int D, int BK, int BV, bool F32>
 __global__ __launch_bounds__(256, 2) void k_mx_rows_both(const MxAttnParams prefix, const MxAttnParams own, int prefix_blocks) {
   __shared__ __attribute__((aligned(16))) ManyShared<D, F32> lds;
